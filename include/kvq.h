@@ -56,7 +56,7 @@ typedef enum {
   KVQ_EINVAL = -1,        /* bad argument: null pointer, bad shape, misalignment, bad clip */
   KVQ_EUNSUPPORTED = -2,  /* valid request outside what is implemented (head_dim != 128, ...) */
   KVQ_ECUDA = -3,         /* a CUDA runtime call failed (launch error, no device, ...) */
-  KVQ_EDEVICE_FLAG = -4   /* a kernel met an out-of-range block-table entry or length */
+  KVQ_EDEVICE_FLAG = -4   /* a kernel met an out-of-range block-table entry, length, page plan or draft tree */
 } kvq_status;
 
 typedef enum {
@@ -291,6 +291,91 @@ kvq_status kvq_decode_step_win(const kvq_layout* layout, int n_seqs, const void*
                                const float* mu_k, float clip_k, float clip_v, uint8_t* pool, const kvq_window* win,
                                int n_splits, void* workspace, size_t workspace_bytes, float* o_rot,
                                kvq_stream stream);
+
+/* ---- Speculative decoding and cross attention over the cache (serving loops around the paged cache of
+ * "Output-Aware Rotation for INT2 KV-Cache Quantization", §6; the paper has no counterpart).
+ * One verification step: kvq_plan_pages grows every request by its drafts, kvq_quantize_append writes the
+ * drafts' keys and values behind the cached tokens, kvq_tree_attention reads cache and drafts for all of
+ * them, and once the accepted path is known kvq_tree_commit moves its records to the front and
+ * kvq_plan_pages gives the rejected drafts' pages back.  A draft attends to itself and its ancestors as
+ * quantized, as kvq_decode_step does for its new token, so that verification and one-token decoding read
+ * the same cache.  BF16 windows (kvq_window) take no part in these calls. */
+
+/* Workspace bytes of kvq_plan_pages. */
+kvq_status kvq_plan_workspace_size(int n_seqs, size_t* bytes);
+
+/* Block tables, free pages and slots for requests whose lengths change, on the device.
+ * Sequence b goes from old_lens[b] to new_lens[b] tokens, either way; with p(x) = ceil(x / page_tokens) it takes pages
+ * p(old) .. p(new) - 1 or gives pages p(new) .. p(old) - 1 back.
+ *   free_ring: int32 [num_blocks], a ring of free page ids: entries head .. tail - 1, modulo num_blocks, are free
+ *   ring_in:   int64 [2] = (head, tail), 0 <= head <= tail <= head + num_blocks; they only ever grow
+ *   ring_out:  int64 [2] (written; not ring_in): head + pages taken, tail + pages given back
+ *   block_table: int32 [n_seqs][max_blocks_per_seq], in place: taken pages are written in (sequence, page) order from
+ *              the head on; given pages go to the tail in the same order, and their entries (as all others) keep their value
+ *   cu_new:    int32 [n_seqs + 1] (written): running sum of max(0, new - old), ready for kvq_quantize_append
+ *              (start_pos = old_lens) and as cu_q of kvq_tree_attention
+ *   slot_map:  int64 [max_new] (written; may be NULL if max_new is 0): new token t of b, at position
+ *              pos = old_lens[b] + t - cu_new[b], has slot page * page_tokens + pos % page_tokens of the pool;
+ *              -1 from cu_new[n_seqs] on
+ *   workspace: >= kvq_plan_workspace_size bytes, 16-byte aligned
+ * Pages given back in a call serve the next one.  A plan that cannot be carried out as a whole (a length outside
+ * [0, max_blocks_per_seq * page_tokens], too few free pages, counters out of range, more new tokens than max_new, more
+ * free pages than num_blocks) changes nothing: cu_new is all 0, slot_map all -1, ring_out = ring_in, and
+ * kvq_device_check reports it.  A page id outside the pool is passed on as it is and flagged; its slots are -1.
+ * n_seqs <= 65535; max_new >= 0. */
+kvq_status kvq_plan_pages(const kvq_layout* layout, int n_seqs, const int32_t* old_lens, const int32_t* new_lens,
+                          int32_t* block_table, int32_t* free_ring, const int64_t* ring_in, int64_t* ring_out,
+                          int max_new, int32_t* cu_new, int64_t* slot_map, void* workspace, size_t workspace_bytes,
+                          kvq_stream stream);
+
+/* Workspace bytes of kvq_tree_attention and kvq_cross_attention (host arithmetic on the arguments). */
+kvq_status kvq_query_block_workspace_size(const kvq_layout* layout, int n_seqs, int n_q_total, int max_q,
+                                          int max_seq_len, size_t* bytes);
+
+/* Attention of every sequence's drafted tokens over the cache and over one another.
+ * Sequence b has n = cu_q[b + 1] - cu_q[b] drafts, whose keys and values are the last n of its seq_lens[b] cached
+ * tokens: draft i at position seq_lens[b] - n + i.  Draft i sees every earlier cached token, itself and its ancestors:
+ *   a_s = (q R_K,h) . (zero_s + scale_s * codeK_s) / sqrt(128),  p = softmax of a over the visible s
+ *   o_rot = sum_s p_s (zero_s + scale_s * codeV_s)          (rotated-V basis, for kvq_out_proj)
+ *   q:        [n_q_total][n_q_heads][128] of q_dtype, the drafts of sequence b in rows cu_q[b] .. cu_q[b + 1] - 1
+ *   cu_q:     int32 [n_seqs + 1], non-decreasing, cu_q[0] >= 0, cu_q[n_seqs] <= n_q_total; rows of no sequence keep their output
+ *   max_q:    (host) >= every n
+ *   parents:  int32 [n_q_total]: the parent of draft i, as an index into the sequence's drafts below i, or -1 for a
+ *             draft that follows the cached tokens; max_q <= 1024.  NULL: a chain, draft i follows i - 1 (a causal
+ *             chunk of a prompt), any number
+ *   seq_lens: int32 [n_seqs], the cached tokens with the drafts; max_seq_len (host) >= every seq_lens[b]
+ *   o_rot:    float [n_q_total][n_q_heads][128] (written)
+ *   workspace: >= kvq_query_block_workspace_size bytes, 16-byte aligned; one call at a time may use it
+ * Results do not depend on timing.  Sequences with inconsistent lengths and out-of-range block ids are flagged
+ * (kvq_device_check) and their outputs are unspecified; a bad parent is flagged and taken as -1.
+ * n_seqs <= 65535; query heads per KV head 1, 2, 4 or 8. */
+kvq_status kvq_tree_attention(const kvq_layout* layout, int n_seqs, int n_q_total, const void* q, kvq_dtype q_dtype,
+                              const int32_t* cu_q, int max_q, const int32_t* parents, const int32_t* seq_lens,
+                              int max_seq_len, const int32_t* block_table, kvq_rot rot_k, const uint8_t* pool,
+                              void* workspace, size_t workspace_bytes, float* o_rot, kvq_stream stream);
+
+/* Cross attention: the queries of sequence b (rows cu_q[b] .. cu_q[b + 1] - 1, any number up to max_q) over all
+ * state_lens[b] cached states, an encoder's keys and values written by kvq_quantize_append, without a mask.
+ * state_lens[b] = 0 gives zero vectors.  Formulas, other arguments, limits and errors as kvq_tree_attention. */
+kvq_status kvq_cross_attention(const kvq_layout* layout, int n_seqs, int n_q_total, const void* q, kvq_dtype q_dtype,
+                               const int32_t* cu_q, int max_q, const int32_t* state_lens, int max_state_len,
+                               const int32_t* block_table, kvq_rot rot_k, const uint8_t* pool, void* workspace,
+                               size_t workspace_bytes, float* o_rot, kvq_stream stream);
+
+/* The accepted drafts of every sequence become cached tokens: the records (codes, scale, zero; every KV head) of
+ * drafts accepted[b][0 .. n_accepted[b] - 1] move, unchanged, to the places of drafts 0 .. n_accepted[b] - 1, so that
+ * the first new_lens[b] = seq_lens[b] - n + n_accepted[b] positions are the sequence.  Follow it with kvq_plan_pages
+ * (seq_lens -> new_lens).
+ *   cu_q:       int32 [n_seqs + 1] as in kvq_tree_attention (cu_new of the plan that grew the sequences)
+ *   accepted:   int32 [n_seqs][max_accept], strictly increasing draft indices, a root-to-leaf path
+ *   n_accepted: int32 [n_seqs], each <= max_accept and <= n
+ *   slot_map:   int64 [n_q_total], the drafts' slots (from kvq_plan_pages)
+ *   seq_lens, new_lens: int32 [n_seqs] (not the same array); new_lens is written
+ *   pool:       in place
+ * A path that is not valid is flagged and taken as empty; a slot outside the pool is flagged and its move left out. */
+kvq_status kvq_tree_commit(const kvq_layout* layout, int n_seqs, int n_q_total, int max_accept, const int32_t* cu_q,
+                           const int32_t* accepted, const int32_t* n_accepted, const int64_t* slot_map,
+                           const int32_t* seq_lens, int32_t* new_lens, uint8_t* pool, kvq_stream stream);
 
 /* The same decode attention for callers that cannot allocate device memory
  * (the paper has no counterpart; this is a deployment convenience).

@@ -101,6 +101,12 @@ def lib() -> ctypes.CDLL:
                                      vp, vp], st),
             "kvq_decode_workspace_size_win": ([lp, i, i, i, wp, ctypes.POINTER(sz)], st),
             "kvq_decode_attention_win": ([lp, i, vp, i, vp, i, vp, KvqRot, KvqRot, vp, wp, i, vp, sz, vp, vp], st),
+            "kvq_plan_workspace_size": ([i, ctypes.POINTER(sz)], st),
+            "kvq_plan_pages": ([lp, i, vp, vp, vp, vp, vp, vp, i, vp, vp, vp, sz, vp], st),
+            "kvq_query_block_workspace_size": ([lp, i, i, i, i, ctypes.POINTER(sz)], st),
+            "kvq_tree_attention": ([lp, i, i, vp, i, vp, i, vp, vp, i, vp, KvqRot, vp, vp, sz, vp, vp], st),
+            "kvq_cross_attention": ([lp, i, i, vp, i, vp, i, vp, i, vp, KvqRot, vp, vp, sz, vp, vp], st),
+            "kvq_tree_commit": ([lp, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp], st),
             "kvq_fold_wo": ([i, i, i, vp, i, KvqRot, vp, i, vp], st),
             "kvq_out_proj": ([i, i, i, vp, vp, i, vp, vp], st),
             "kvq_wo_packed_bytes": ([i, i, ctypes.POINTER(sz)], st),
@@ -128,7 +134,8 @@ def lib() -> ctypes.CDLL:
 EXPORTED = ("kvq_last_error", "kvq_pool_bytes", "kvq_device_check", "kvq_key_mean", "kvq_rotate_heads",
             "kvq_quantize_append", "kvq_decode_workspace_size", "kvq_decode_attention",
             "kvq_decode_attention_noalloc", "kvq_decode_step", "kvq_decode_step_win", "kvq_window_append", "kvq_decode_workspace_size_win",
-            "kvq_decode_attention_win", "kvq_fold_wo",
+            "kvq_decode_attention_win", "kvq_plan_workspace_size", "kvq_plan_pages", "kvq_query_block_workspace_size",
+            "kvq_tree_attention", "kvq_cross_attention", "kvq_tree_commit", "kvq_fold_wo",
             "kvq_out_proj", "kvq_wo_packed_bytes", "kvq_pack_wo", "kvq_out_proj_packed", "kvq_calib_workspace_size", "kvq_calib_nmse", "kvq_report_workspace_size",
             "kvq_head_error_report", "kvq_optr_workspace_size", "kvq_optr_loss_grad", "kvq_optr_calibrate_head")
 
@@ -320,6 +327,99 @@ def kvq_decode_attention_win(layout: KvqLayout, q, seq_lens, max_seq_len: int, b
                                           _win_ref(win), n_splits, _ptr(workspace),
                                           workspace.numel() * workspace.element_size(), _ptr(o_rot),
                                           _stream(stream)))
+
+
+# ---- speculative decoding and cross attention over the cache ----
+def _dense(t, name: str, dtype, shape):
+    """A dense tensor of this type and shape (None in the shape: any size) on the current CUDA device."""
+    import torch
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return _ptr(_contig(t, name))
+
+
+def _pool(layout: KvqLayout, pool):
+    """The cache pool: uint8 of any shape, no smaller than the layout's."""
+    import torch
+    if pool.numel() < kvq_pool_bytes(layout):
+        raise ValueError(f"pool has {pool.numel()} bytes, the layout needs {kvq_pool_bytes(layout)}")
+    return _dense(pool, "pool", torch.uint8, tuple(pool.shape))
+
+
+def kvq_plan_workspace_size(n_seqs: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().kvq_plan_workspace_size(n_seqs, ctypes.byref(out)))
+    return int(out.value)
+
+
+def kvq_plan_pages(layout: KvqLayout, old_lens, new_lens, block_table, free_ring, ring_in, ring_out, cu_new, slot_map,
+                   workspace, stream=None) -> None:
+    """Takes and gives back pages for requests going from old_lens to new_lens tokens: block_table and the ring of
+    free pages in place (counters (head, tail): ring_in -> ring_out, int64 [2]); cu_new int32 [n + 1] and slot_map
+    int64 [capacity for new tokens] are written.  See include/kvq.h."""
+    import torch
+    n, i32, i64 = old_lens.shape[0], torch.int32, torch.int64
+    _check(lib().kvq_plan_pages(
+        ctypes.byref(layout), n, _dense(old_lens, "old_lens", i32, (n,)), _dense(new_lens, "new_lens", i32, (n,)),
+        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq)),
+        _dense(free_ring, "free_ring", i32, (layout.num_blocks,)), _dense(ring_in, "ring_in", i64, (2,)),
+        _dense(ring_out, "ring_out", i64, (2,)), slot_map.shape[0], _dense(cu_new, "cu_new", i32, (n + 1,)),
+        _dense(slot_map, "slot_map", i64, (None,)), _dense(workspace, "workspace", torch.uint8, (None,)),
+        workspace.numel(), _stream(stream)))
+
+
+def kvq_query_block_workspace_size(layout: KvqLayout, n_seqs: int, n_q_total: int, max_q: int, max_seq_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().kvq_query_block_workspace_size(ctypes.byref(layout), n_seqs, n_q_total, max_q, max_seq_len,
+                                                ctypes.byref(out)))
+    return int(out.value)
+
+
+def kvq_tree_attention(layout: KvqLayout, q, cu_q, max_q: int, parents, seq_lens, max_seq_len: int, block_table,
+                       rot_k: DeviceRot, pool, workspace, o_rot, stream=None) -> None:
+    """Attention of every sequence's drafts (q [n_q_total, H_q, 128], rows cu_q[b] .. cu_q[b + 1]) over the cache and
+    over their own ancestors; the drafts are the last of the seq_lens[b] cached tokens.  parents: int32 [n_q_total]
+    (index within the sequence, -1: follows the cache), or None for a chain (a causal chunk).  o_rot: fp32 like q."""
+    import torch
+    n, total, i32 = seq_lens.shape[0], q.shape[0], torch.int32
+    _check(lib().kvq_tree_attention(
+        ctypes.byref(layout), n, total, _dense(q, "q", q.dtype, (total, layout.n_q_heads, HEAD_DIM)), _dtype_code(q),
+        _dense(cu_q, "cu_q", i32, (n + 1,)), max_q,
+        None if parents is None else _dense(parents, "parents", i32, (total,)),
+        _dense(seq_lens, "seq_lens", i32, (n,)), max_seq_len,
+        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq)), rot_k.c, _pool(layout, pool),
+        _dense(workspace, "workspace", torch.uint8, (None,)), workspace.numel(),
+        _dense(o_rot, "o_rot", torch.float32, (total, layout.n_q_heads, HEAD_DIM)), _stream(stream)))
+
+
+def kvq_cross_attention(layout: KvqLayout, q, cu_q, max_q: int, state_lens, max_state_len: int, block_table,
+                        rot_k: DeviceRot, pool, workspace, o_rot, stream=None) -> None:
+    """Attention of query blocks over all cached states of their sequence (an encoder's), without a mask."""
+    import torch
+    n, total, i32 = state_lens.shape[0], q.shape[0], torch.int32
+    _check(lib().kvq_cross_attention(
+        ctypes.byref(layout), n, total, _dense(q, "q", q.dtype, (total, layout.n_q_heads, HEAD_DIM)), _dtype_code(q),
+        _dense(cu_q, "cu_q", i32, (n + 1,)), max_q, _dense(state_lens, "state_lens", i32, (n,)), max_state_len,
+        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq)), rot_k.c, _pool(layout, pool),
+        _dense(workspace, "workspace", torch.uint8, (None,)), workspace.numel(),
+        _dense(o_rot, "o_rot", torch.float32, (total, layout.n_q_heads, HEAD_DIM)), _stream(stream)))
+
+
+def kvq_tree_commit(layout: KvqLayout, cu_q, accepted, n_accepted, slot_map, seq_lens, new_lens, pool,
+                    stream=None) -> None:
+    """Moves the accepted drafts' records (accepted int32 [n, max_accept], increasing; n_accepted int32 [n]) to the
+    places of the first drafts and writes new_lens = seq_lens - drafts + accepted."""
+    import torch
+    n, i32 = seq_lens.shape[0], torch.int32
+    _check(lib().kvq_tree_commit(
+        ctypes.byref(layout), n, slot_map.shape[0], accepted.shape[1], _dense(cu_q, "cu_q", i32, (n + 1,)),
+        _dense(accepted, "accepted", i32, (n, None)), _dense(n_accepted, "n_accepted", i32, (n,)),
+        _dense(slot_map, "slot_map", torch.int64, (None,)), _dense(seq_lens, "seq_lens", i32, (n,)),
+        _dense(new_lens, "new_lens", i32, (n,)), _pool(layout, pool), _stream(stream)))
 
 
 def kvq_fold_wo(w_o, n_q_heads: int, n_kv_heads: int, rot_v: DeviceRot, w_folded, stream=None) -> None:

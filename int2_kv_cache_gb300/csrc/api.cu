@@ -171,10 +171,12 @@ kvq_status kvq_device_check(kvq_stream stream) {
   const unsigned zero = 0;
   e = cudaMemcpy(addr, &zero, sizeof(zero), cudaMemcpyHostToDevice);
   if (e != cudaSuccess) return cuda_fail(e, "clear device error word");
-  return fail(KVQ_EDEVICE_FLAG, "kernel bounds check fired (0x%x):%s%s%s", word,
+  return fail(KVQ_EDEVICE_FLAG, "kernel bounds check fired (0x%x):%s%s%s%s%s", word,
               (word & kvq::ERR_BLOCK_RANGE) ? " block-table entry out of range;" : "",
               (word & kvq::ERR_POS_RANGE) ? " position beyond the block table;" : "",
-              (word & kvq::ERR_SEQ_RANGE) ? " inconsistent cu_new/seq_lens;" : "");
+              (word & kvq::ERR_SEQ_RANGE) ? " inconsistent cu_new/seq_lens;" : "",
+              (word & kvq::ERR_PLAN) ? " page plan not carried out (lengths, free pages, ring counters or max_new);" : "",
+              (word & kvq::ERR_TREE) ? " draft parent or accepted path not valid;" : "");
 }
 
 kvq_status kvq_key_mean(int n_tok, int n_kv_heads, const void* k, kvq_dtype dtype, float* mu,
@@ -635,6 +637,131 @@ kvq_status kvq_head_error_report(int n_tok, int n_qpos, int n_kv_heads, int gqa,
                                           kvq::to_dev(rot_k), kvq::to_dev(rot_v), mu, clip_k, clip_v, out,
                                           workspace, err, stream);
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "kvq_head_error_report");
+}
+
+kvq_status kvq_plan_workspace_size(int n_seqs, size_t* bytes) {
+  if (!bytes) return fail(KVQ_EINVAL, "bytes is NULL");
+  if (n_seqs < 1 || n_seqs > 65535) return fail(KVQ_EINVAL, "n_seqs %d outside [1, 65535]", n_seqs);
+  *bytes = kvq::plan_workspace_bytes(n_seqs);
+  return KVQ_OK;
+}
+
+kvq_status kvq_plan_pages(const kvq_layout* layout, int n_seqs, const int32_t* old_lens, const int32_t* new_lens,
+                          int32_t* block_table, int32_t* free_ring, const int64_t* ring_in, int64_t* ring_out,
+                          int max_new, int32_t* cu_new, int64_t* slot_map, void* workspace, size_t workspace_bytes,
+                          kvq_stream stream) {
+  KVQ_CHECK(check_layout(layout, false));
+  size_t need = 0;
+  KVQ_CHECK(kvq_plan_workspace_size(n_seqs, &need));
+  if (max_new < 0) return fail(KVQ_EINVAL, "max_new %d < 0", max_new);
+  if ((long long)layout->max_blocks_per_seq * layout->page_tokens >= (1ll << 31))
+    return fail(KVQ_EUNSUPPORTED, "max_blocks_per_seq * page_tokens >= 2^31");
+  KVQ_IDX(old_lens, "old_lens");
+  KVQ_IDX(new_lens, "new_lens");
+  KVQ_IDX(block_table, "block_table");
+  KVQ_IDX(free_ring, "free_ring");
+  KVQ_PTR(ring_in, "ring_in");
+  KVQ_PTR(ring_out, "ring_out");
+  if (ring_in == ring_out) return fail(KVQ_EINVAL, "ring_in and ring_out must not alias");
+  KVQ_IDX(cu_new, "cu_new");
+  if (max_new > 0) KVQ_PTR(slot_map, "slot_map");
+  KVQ_PTR(workspace, "workspace");
+  if (workspace_bytes < need) return fail(KVQ_EINVAL, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  unsigned* err = nullptr;
+  KVQ_CHECK(device_error_word(&err));
+  cudaError_t e = kvq::launch_plan_pages(geom(layout), n_seqs, old_lens, new_lens, block_table, free_ring, ring_in,
+                                         ring_out, max_new, cu_new, slot_map, workspace, err, stream);
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "kvq_plan_pages");
+}
+
+static kvq_status check_query_block(const kvq_layout* layout, int n_seqs, int n_q_total, int max_q, int max_seq_len) {
+  KVQ_CHECK(check_layout(layout, true));
+  if (n_seqs < 0 || n_q_total < 0 || max_q < 0 || max_seq_len < 0)
+    return fail(KVQ_EINVAL, "bad n_seqs %d / n_q_total %d / max_q %d / max_seq_len %d", n_seqs, n_q_total, max_q,
+                max_seq_len);
+  if ((long long)n_q_total * layout->n_q_heads >= (1ll << 31))
+    return fail(KVQ_EUNSUPPORTED, "n_q_total * n_q_heads >= 2^31");
+  return check_decode_size(layout, n_seqs, max_seq_len);
+}
+
+kvq_status kvq_query_block_workspace_size(const kvq_layout* layout, int n_seqs, int n_q_total, int max_q,
+                                          int max_seq_len, size_t* bytes) {
+  if (!bytes) return fail(KVQ_EINVAL, "bytes is NULL");
+  KVQ_CHECK(check_query_block(layout, n_seqs, n_q_total, max_q, max_seq_len));
+  *bytes = kvq::query_block_workspace_bytes(n_seqs, layout->n_q_heads, layout->n_kv_heads, n_q_total, max_q, max_seq_len);
+  return KVQ_OK;
+}
+
+static kvq_status query_block_impl(const char* name, int mode, const kvq_layout* layout, int n_seqs, int n_q_total,
+                                   const void* q, kvq_dtype q_dtype, const int32_t* cu_q, int max_q,
+                                   const int32_t* parents, const int32_t* lens, int max_len,
+                                   const int32_t* block_table, kvq_rot rot_k, const uint8_t* pool, void* workspace,
+                                   size_t workspace_bytes, float* o_rot, kvq_stream stream) {
+  size_t need = 0;
+  KVQ_CHECK(kvq_query_block_workspace_size(layout, n_seqs, n_q_total, max_q, max_len, &need));
+  if ((long long)max_len > (long long)layout->max_blocks_per_seq * layout->page_tokens)
+    return fail(KVQ_EINVAL, "max_seq_len %d outside [0, max_blocks_per_seq * page_tokens]", max_len);
+  if (!valid_dtype(q_dtype)) return fail(KVQ_EINVAL, "bad q dtype %d", (int)q_dtype);
+  if (mode == kvq::QB_TREE && max_q > kvq::QB_MAX_TREE)
+    return fail(KVQ_EUNSUPPORTED, "max_q %d: trees of up to %d drafts are supported", max_q, kvq::QB_MAX_TREE);
+  KVQ_CHECK(check_rot(rot_k, "rot_k"));
+  if (n_seqs == 0 || n_q_total == 0 || max_q == 0) return KVQ_OK;
+  KVQ_PTR(q, "q");
+  KVQ_IDX(cu_q, "cu_q");
+  if (mode == kvq::QB_TREE) KVQ_IDX(parents, "parents");
+  KVQ_IDX(lens, "lens");
+  KVQ_IDX(block_table, "block_table");
+  KVQ_PTR(pool, "pool");
+  KVQ_PTR(o_rot, "o_rot");
+  KVQ_PTR(workspace, "workspace");
+  if (workspace_bytes < need) return fail(KVQ_EINVAL, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  unsigned* err = nullptr;
+  KVQ_CHECK(device_error_word(&err));
+  cudaError_t e = kvq::launch_query_block(geom(layout), layout->n_q_heads, n_seqs, n_q_total, q, q_dtype, cu_q, max_q,
+                                          parents, mode, lens, max_len, block_table, kvq::to_dev(rot_k), pool,
+                                          workspace, o_rot, err, stream);
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e, name);
+}
+
+kvq_status kvq_tree_attention(const kvq_layout* layout, int n_seqs, int n_q_total, const void* q, kvq_dtype q_dtype,
+                              const int32_t* cu_q, int max_q, const int32_t* parents, const int32_t* seq_lens,
+                              int max_seq_len, const int32_t* block_table, kvq_rot rot_k, const uint8_t* pool,
+                              void* workspace, size_t workspace_bytes, float* o_rot, kvq_stream stream) {
+  return query_block_impl("kvq_tree_attention", parents ? kvq::QB_TREE : kvq::QB_CHAIN, layout, n_seqs, n_q_total, q,
+                          q_dtype, cu_q, max_q, parents, seq_lens, max_seq_len, block_table, rot_k, pool, workspace,
+                          workspace_bytes, o_rot, stream);
+}
+
+kvq_status kvq_cross_attention(const kvq_layout* layout, int n_seqs, int n_q_total, const void* q, kvq_dtype q_dtype,
+                               const int32_t* cu_q, int max_q, const int32_t* state_lens, int max_state_len,
+                               const int32_t* block_table, kvq_rot rot_k, const uint8_t* pool, void* workspace,
+                               size_t workspace_bytes, float* o_rot, kvq_stream stream) {
+  return query_block_impl("kvq_cross_attention", kvq::QB_CROSS, layout, n_seqs, n_q_total, q, q_dtype, cu_q, max_q,
+                          nullptr, state_lens, max_state_len, block_table, rot_k, pool, workspace, workspace_bytes,
+                          o_rot, stream);
+}
+
+kvq_status kvq_tree_commit(const kvq_layout* layout, int n_seqs, int n_q_total, int max_accept, const int32_t* cu_q,
+                           const int32_t* accepted, const int32_t* n_accepted, const int64_t* slot_map,
+                           const int32_t* seq_lens, int32_t* new_lens, uint8_t* pool, kvq_stream stream) {
+  KVQ_CHECK(check_layout(layout, false));
+  if (n_seqs < 0 || n_q_total < 0 || max_accept < 0)
+    return fail(KVQ_EINVAL, "bad n_seqs %d / n_q_total %d / max_accept %d", n_seqs, n_q_total, max_accept);
+  if (n_seqs > 65535) return fail(KVQ_EUNSUPPORTED, "n_seqs %d > 65535", n_seqs);
+  if (n_seqs == 0) return KVQ_OK;
+  KVQ_IDX(cu_q, "cu_q");
+  if (max_accept > 0) KVQ_IDX(accepted, "accepted");
+  KVQ_IDX(n_accepted, "n_accepted");
+  if (n_q_total > 0) KVQ_PTR(slot_map, "slot_map");
+  KVQ_IDX(seq_lens, "seq_lens");
+  KVQ_IDX(new_lens, "new_lens");
+  if (seq_lens == new_lens) return fail(KVQ_EINVAL, "seq_lens and new_lens must not alias");
+  KVQ_PTR(pool, "pool");
+  unsigned* err = nullptr;
+  KVQ_CHECK(device_error_word(&err));
+  cudaError_t e = kvq::launch_tree_commit(geom(layout), n_seqs, n_q_total, max_accept, cu_q, accepted, n_accepted,
+                                          slot_map, seq_lens, new_lens, pool, err, stream);
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e, "kvq_tree_commit");
 }
 
 }  // extern "C"

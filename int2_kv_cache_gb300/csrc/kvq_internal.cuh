@@ -22,6 +22,8 @@ enum : unsigned {
   ERR_POS_RANGE = 2u,     // position beyond max_blocks_per_seq * page_tokens
   ERR_SEQ_RANGE = 4u,     // cu_new / seq_lens inconsistent (negative, decreasing, too long)
   ERR_TIMEOUT = 8u,       // a bounded wait on a shared-memory copy gave up
+  ERR_PLAN = 16u,         // a page plan that cannot be carried out (lengths, free pages, ring, max_new)
+  ERR_TREE = 32u,         // a draft's parent or an accepted path is not valid
 };
 
 struct RotDev {
@@ -166,6 +168,24 @@ size_t wo_packed_bytes(int d_model, int k_dim);
 cudaError_t launch_pack_wo(int d_model, int k_dim, const void* w, void* out, cudaStream_t s);
 cudaError_t launch_out_proj_packed(int n_rows, int d_model, int k_dim, const float* x, const void* w_packed, float* y,
                                    unsigned* err, cudaStream_t s);
+
+// page_plan.cu
+size_t plan_workspace_bytes(int n_seqs);
+cudaError_t launch_plan_pages(const PageGeom& g, int n_seqs, const int32_t* old_lens, const int32_t* new_lens,
+                              int32_t* table, int32_t* ring, const int64_t* ring_in, int64_t* ring_out, int max_new,
+                              int32_t* cu_new, int64_t* slots, void* ws, unsigned* err, cudaStream_t s);
+cudaError_t launch_tree_commit(const PageGeom& g, int n_seqs, int n_total, int max_accept, const int32_t* cu_q,
+                               const int32_t* accepted, const int32_t* n_accepted, const int64_t* slots,
+                               const int32_t* lens, int32_t* new_lens, uint8_t* pool, unsigned* err, cudaStream_t s);
+
+// query_block.cu: what a query sees of the last cached positions of its sequence
+enum { QB_CROSS = 0, QB_CHAIN = 1, QB_TREE = 2 };  // everything; those up to its own; its ancestors and itself
+constexpr int QB_MAX_TREE = 1024;                  // drafts a sequence in a tree
+size_t query_block_workspace_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int n_total, int max_q, int max_len);
+cudaError_t launch_query_block(const PageGeom& g, int n_q_heads, int n_seqs, int n_total, const void* q, int dtype,
+                               const int32_t* cu_q, int max_q, const int32_t* parents, int mode, const int32_t* lens,
+                               int max_len, const int32_t* table, RotDev rot_k, const uint8_t* pool, void* ws,
+                               float* o_rot, unsigned* err, cudaStream_t s);
 
 // optr.cu: OptR calibration of one KV head (fp64)
 struct OptrTraceIn {  // one trace of the head: q [n_qpos][gqa][128], k, v [n_tok][128] (fp32)

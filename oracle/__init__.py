@@ -31,10 +31,12 @@ numpy, with no blocking, fusion or reordering beyond what the definitions state:
 * ``window``     -- BF16 sink and recent windows beside the INT2 cache (§5
   implementation details, Table A; appendix "OptR Algorithm"): membership, the
   window record layout, bf16 rounding, the windowed decode readout.
+* ``tree``       -- speculative decoding over the cache: a draft tree's visibility, block attention
+  (trees, chains, cross attention), page plans, commits of accepted paths.
 
 Every function here is pinned by ``tests/test_oracle_*.py`` against closed
 forms, library routines, brute force on tiny inputs or constants printed on the
 pages; the page-1 NMSE values (52.35 / 1.96) are the one quantity left
 "parity unpinned" (their generator and data recipe are not published).
 """
-from . import rotations, quant, cache, attention, output, calib, window, report, optr  # noqa: F401
+from . import rotations, quant, cache, attention, output, calib, window, report, optr, tree  # noqa: F401
