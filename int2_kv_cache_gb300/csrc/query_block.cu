@@ -9,49 +9,122 @@
 // tin(a) <= tin(i) < tin(a) + size(a), one unsigned comparison whatever the tree's
 // depth.  A chain (causal chunk) is tin(i) = i, size(i) = n - i.
 //
-// Launches: qb_tree_kernel (trees only) numbers the nodes, qb_rotate_kernel rotates
-// the queries into the workspace (base-2 logits: scaled by log2(e) / sqrt(128)),
-// qb_attend_kernel takes one warp per query row.
-#include "kvq_internal.cuh"
+// Products.  Unlike the single-token decode (bound by the page stream), a block of
+// n queries does 512 n gqa flop per 72 cached bytes, and above about 40 rows a KV
+// head the tensor cores are the bound.  Both products therefore run on tcgen05
+// with the 2-bit codes as the A operand in tensor memory and the queries as the N
+// dimension, so that a block of 16, 32 or 64 rows costs what it holds:
+//   S^T [128 tokens x N]   = C_K [128 tokens x 128 channels] Q'^T [128 x N]
+//   O^T [128 channels x N] = C_V^T [128 channels x 128 tokens] W^T [128 x N]
+// The codes enter centred, c - 1.5 in fp16 (exact): with mid = z + 1.5 s
+//   a_s = s (q' . (c - 1.5)) + mid sum(q'),   o = sum_s (p_s s_s)(c - 1.5) + sum_s p_s mid_s
+// (uncentred codes would put a large positive sum into the accumulators that the z
+// term cancels, and with it the accumulators' rounding).  The fp32 operands q' and
+// w = p s enter as two fp16 halves (hi, and the remainder), 22 bits together, the
+// remainders first: one accumulator takes both.  Each 128-token product starts
+// from zero and is added up in fp32 registers, so no long sum runs through the
+// tensor cores' own rounding.
+// Softmax weights are kept as w = 2^(a + log2 s - M) directly, p = w / s: fp16 then
+// holds w whatever the value scales are (a constant group, s = 0, takes the
+// smallest fp16 as s: its codes are 0 and mid compensates exactly).  M is a lazy
+// reference, 2^8 below a running maximum and moved only when a weight would pass
+// 2^14: one vote a tile, and most tiles never move it.
+//
+// A CTA (18 warps, one per SM, persistent over an equal slice of all tiles):
+//   warps 0-3    expand the codes of a tile into tensor memory: a thread owns a token
+//                (keys) or, through a transposing load, 16 channels of a field (values)
+//   warps 4-11   softmax: a thread owns a token, each half of the warps half of the
+//                rows; weights go to shared memory as the next product's B operand
+//   warps 12-15  add up the 128-token products, load the next unit's queries, write out
+//   warp 16      page copies (cp.async.bulk) and the list of units
+//   warp 17      issues the MMAs
+// A unit is (sequence, KV head, row tile).  Slices cut units: a unit wholly inside a
+// CTA is written out at once, a cut one leaves partials (numerator, l, M) that
+// qb_combine_kernel joins in slice order (results do not depend on timing).
+#include <cstddef>
+
+#include "quant_common.cuh"
+#include "tcgen05.cuh"
 
 namespace kvq {
 
-constexpr float QB_SCALE = 0.12751742902274214f;  // log2(e) / sqrt(128)
+constexpr float QB_SCALE = 0.12751742902274214f;  // log2(e) / sqrt(128): base-2 logits
 
+constexpr int QB_TOK = 128;                       // tokens a tile
+constexpr int QB_STAGES = 4;
+constexpr int QB_STAGE_BYTES = QB_TOK * 72;
+constexpr int QB_THREADS = 18 * 32;
+constexpr int QB_PBUF = QB_TOK * 128;             // one half of W^T: 128 rows of 128 bytes (64 fp16 columns)
+constexpr int QB_UNITS = 4;                       // ring of unit descriptors
+constexpr float QB_LIFT = 8.f, QB_TRIGGER = 14.f; // weights: running maximum at 2^8, moved when one would pass 2^14
+constexpr float QB_NONE = -1e30f;                 // reference of a row that has seen nothing
+
+__host__ __device__ constexpr int qb_smem_bytes(int n) {
+  return 1024 + 2 * n * 512 + 2 * 2 * QB_PBUF + QB_STAGES * QB_STAGE_BYTES;
+}
+
+// ---------------------------------------------------------------------------
+// Workspace and the list of tiles
+// ---------------------------------------------------------------------------
 struct QbWs {
-  float* q;    // [n_total][n_q_heads][128] rotated, scaled queries
-  int2* tree;  // [n_total] (tin, size)
+  float* q;          // [n_total][n_q_heads][128] rotated, scaled queries
+  int2* tree;        // [n_total] (tin, size)
+  long long* tiles;  // [n_seqs + 1] running sum of the sequences' tiles
+  float* part;       // [2 grid][N][130]: numerator [N][128], l [N], M [N]
 };
 
 static size_t qb_align(size_t x) { return (x + 255) & ~size_t(255); }
 
-static size_t qb_layout(void* base, int n_total, int n_q_heads, QbWs* out) {
-  const size_t o_q = 0, o_tree = qb_align((size_t)n_total * n_q_heads * D * sizeof(float));
-  const size_t total = qb_align(o_tree + (size_t)n_total * sizeof(int2));
+// Rows a tile: the smallest of 16, 32, 64 that holds a sequence's rows of one KV head, else 64.
+static int qb_rows(int max_q, int gqa) {
+  const long long r = (long long)max_q * gqa;
+  return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+}
+
+static size_t qb_layout(void* base, int n_seqs, int n_total, int n_q_heads, int rows, int grid, QbWs* out) {
+  const size_t o_tree = qb_align((size_t)n_total * n_q_heads * D * sizeof(float));
+  const size_t o_tiles = qb_align(o_tree + (size_t)n_total * sizeof(int2));
+  const size_t o_part = qb_align(o_tiles + ((size_t)n_seqs + 1) * sizeof(long long));
   if (out) {
-    out->q = reinterpret_cast<float*>(static_cast<char*>(base) + o_q);
-    out->tree = reinterpret_cast<int2*>(static_cast<char*>(base) + o_tree);
+    char* p = static_cast<char*>(base);
+    out->q = reinterpret_cast<float*>(p);
+    out->tree = reinterpret_cast<int2*>(p + o_tree);
+    out->tiles = reinterpret_cast<long long*>(p + o_tiles);
+    out->part = reinterpret_cast<float*>(p + o_part);
   }
-  return total;
+  return qb_align(o_part + (size_t)2 * grid * rows * (D + 2) * sizeof(float));
 }
 
 size_t query_block_workspace_bytes(int n_seqs, int n_q_heads, int n_kv_heads, int n_total, int max_q, int max_len) {
-  return qb_layout(nullptr, n_total, n_q_heads, nullptr);
+  return qb_layout(nullptr, n_seqs, n_total, n_q_heads, qb_rows(max_q, n_q_heads / n_kv_heads), device_sm_count(),
+                   nullptr);
 }
 
 // A sequence's queries [c0, c0 + n) and cached length, checked; n = 0 where they are inconsistent.
 struct QbSeq {
   int c0, n, len;
 };
-__device__ __forceinline__ QbSeq qb_seq(int b, const int32_t* cu_q, const int32_t* lens, int n_total, int max_q,
-                                        int max_len, int mode, unsigned* err) {
+
+struct QbArgs {
+  PageGeom g;
+  int n_q_heads, gqa, n_seqs, n_total, max_q, max_len, mode;
+  const int32_t* cu_q;
+  const int32_t* lens;
+  const int32_t* table;
+  const uint8_t* pool;
+  QbWs ws;
+  float* out;
+  unsigned* err;
+};
+
+__device__ __forceinline__ QbSeq qb_seq(const QbArgs& a, int b, unsigned* err) {
   QbSeq q;
-  q.c0 = cu_q[b];
-  const int end = cu_q[b + 1];
-  q.len = lens[b];
+  q.c0 = a.cu_q[b];
+  const int end = a.cu_q[b + 1];
+  q.len = a.lens[b];
   q.n = end - q.c0;
-  if (q.c0 < 0 || end < q.c0 || end > n_total || q.n > max_q || q.len < 0 || q.len > max_len ||
-      (mode != QB_CROSS && q.n > q.len)) {
+  if (q.c0 < 0 || end < q.c0 || end > a.n_total || q.n > a.max_q || q.len < 0 || q.len > a.max_len ||
+      (a.mode != QB_CROSS && q.n > q.len)) {
     flag_error(err, ERR_SEQ_RANGE);
     q.n = 0;
     q.len = 0;
@@ -59,15 +132,141 @@ __device__ __forceinline__ QbSeq qb_seq(int b, const int32_t* cu_q, const int32_
   return q;
 }
 
-__global__ void __launch_bounds__(256)
-qb_tree_kernel(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ lens, const int32_t* __restrict__ parents,
-               int n_total, int max_q, int max_len, int2* __restrict__ tree, unsigned* err) {
+// Tiles of a sequence.  Row tile j of a causal chunk ends with draft min(n, (j + 1) c) - 1
+// (c = N / gqa drafts a row tile, a power of two) and stops there:
+// ceil((base + (j + 1) c) / 128) = floor((x + j + 1) / m), m = 128 / c, x = floor((base + 127) / c),
+// whose sums have a closed form; trees and cross attention read every tile for each row tile.
+struct QbSpan {
+  int n_rt, nt, lc, lm, x;  // row tiles; tiles of the last (chain) or of every one; log2 c, log2 m
+  bool chain;
+  __device__ __forceinline__ long long floor_sum(long long t) const {  // sum of floor(k / m) for k = 0 .. t
+    const long long q = t >> lm;
+    return ((q * (q - 1) / 2) << lm) + q * (t - (q << lm) + 1);
+  }
+  // tiles of the row tiles before j, one KV head
+  __device__ __forceinline__ long long before(int j) const {
+    return chain ? floor_sum((long long)x + j) - floor_sum(x) : (long long)nt * j;
+  }
+  __device__ __forceinline__ int tiles(int j) const { return chain && j + 1 < n_rt ? (x + j + 1) >> lm : nt; }
+  __device__ __forceinline__ long long total() const { return n_rt ? before(n_rt - 1) + nt : 0; }
+};
+
+template <int N>
+__device__ __forceinline__ QbSpan qb_span(const QbArgs& a, const QbSeq& q) {
+  QbSpan s;
+  s.lc = 31 - __clz(N / a.gqa);
+  s.lm = 7 - s.lc;
+  s.n_rt = (int)(((long long)q.n * a.gqa + N - 1) / N);
+  s.nt = q.len ? (q.len + QB_TOK - 1) / QB_TOK : 1;
+  s.chain = a.mode == QB_CHAIN;
+  s.x = (q.len - q.n + 127) >> s.lc;
+  return s;
+}
+
+struct QbUnit {
+  int b, rt, h;
+  int c0, n, len;     // the sequence
+  int t0, t1, nt;     // tiles [t0, t1) of nt in this slice
+};
+
+// The unit that holds tile `t` of all, by one warp; u.t0 = the tile inside the unit.
+template <int N>
+__device__ __forceinline__ QbUnit qb_locate(const QbArgs& a, long long t, int lane) {
+  int lo = 0, cnt = a.n_seqs;
+  while (cnt > 1) {  // the last sequence that starts at or before t
+    const int step = (cnt + 31) / 32, i = lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, i < cnt && a.ws.tiles[lo + i] <= t);
+    const int k = 31 - __clz(m);
+    lo += k * step;
+    cnt = min(step, cnt - k * step);
+  }
+  QbUnit u;
+  u.b = lo;
+  const QbSeq q = qb_seq(a, lo, nullptr);
+  const QbSpan s = qb_span<N>(a, q);
+  const int H = a.g.n_kv_heads;
+  const long long rem = t - a.ws.tiles[lo];
+  int j0 = 0, j1 = s.n_rt;
+  while (j1 - j0 > 1) {
+    const int mid = (j0 + j1) >> 1;
+    if (s.before(mid) * H <= rem) j0 = mid;
+    else j1 = mid;
+  }
+  u.rt = j0;
+  u.nt = s.tiles(j0);
+  const long long in = rem - s.before(j0) * H;
+  u.h = (int)(in / u.nt);
+  u.t0 = (int)(in % u.nt);
+  u.t1 = u.nt;
+  u.c0 = q.c0;
+  u.n = q.n;
+  u.len = q.len;
+  return u;
+}
+
+// The unit after u, from its first tile.
+template <int N>
+__device__ __forceinline__ void qb_next(const QbArgs& a, QbUnit& u) {
+  QbSeq q{u.c0, u.n, u.len};
+  if (++u.h == a.g.n_kv_heads) {
+    u.h = 0;
+    if (++u.rt >= qb_span<N>(a, q).n_rt) {
+      u.rt = 0;
+      do {
+        if (++u.b >= a.n_seqs) {
+          u.nt = 0;
+          return;
+        }
+        q = qb_seq(a, u.b, nullptr);
+      } while (q.n == 0);
+      u.c0 = q.c0;
+      u.n = q.n;
+      u.len = q.len;
+    }
+  }
+  u.nt = qb_span<N>(a, q).tiles(u.rt);
+  u.t0 = 0;
+  u.t1 = u.nt;
+}
+
+// ---------------------------------------------------------------------------
+// Preparation: one launch for the list of tiles (block 0), the trees' numbering (one
+// block a sequence) and the rotation of the queries (a warp a row).
+// ---------------------------------------------------------------------------
+constexpr int QB_PREP_THREADS = 256;
+
+template <int N>
+__device__ __forceinline__ void qb_list_tiles(const QbArgs& a) {
+  __shared__ long long s_warp[QB_PREP_THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (a.n_seqs + QB_PREP_THREADS - 1) / QB_PREP_THREADS;
+  const int b0 = min(a.n_seqs, (int)threadIdx.x * per), b1 = min(a.n_seqs, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += qb_span<N>(a, qb_seq(a, b, a.err)).total() * a.g.n_kv_heads;
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  long long at = inc - mine;
+  for (int w = 0; w < warp; ++w) at += s_warp[w];
+  for (int b = b0; b < b1; ++b) {
+    a.ws.tiles[b] = at;
+    at += qb_span<N>(a, qb_seq(a, b, nullptr)).total() * a.g.n_kv_heads;
+  }
+  if (threadIdx.x == QB_PREP_THREADS - 1) a.ws.tiles[a.n_seqs] = at;
+}
+
+__device__ __forceinline__ void qb_number_tree(const QbArgs& a, int b, const int32_t* __restrict__ parents) {
   __shared__ int s_par[QB_MAX_TREE], s_size[QB_MAX_TREE], s_off[QB_MAX_TREE];
-  const QbSeq q = qb_seq(blockIdx.x, cu_q, lens, n_total, max_q, max_len, QB_TREE, err);
+  const QbSeq q = qb_seq(a, b, nullptr);
   for (int i = threadIdx.x; i < q.n; i += blockDim.x) {
     int p = parents[q.c0 + i];
     if (p < -1 || p >= i) {
-      flag_error(err, ERR_TREE);
+      flag_error(a.err, ERR_TREE);
       p = -1;
     }
     s_par[i] = p;
@@ -88,19 +287,14 @@ qb_tree_kernel(const int32_t* __restrict__ cu_q, const int32_t* __restrict__ len
   for (int i = threadIdx.x; i < q.n; i += blockDim.x) {
     int tin = -1;
     for (int j = i; j >= 0; j = s_par[j]) tin += s_off[j];
-    tree[q.c0 + i] = make_int2(tin, s_size[i]);
+    a.ws.tree[q.c0 + i] = make_int2(tin, s_size[i]);
   }
 }
 
 // One warp a row (token, query head): y = x R * scale.
-__global__ void __launch_bounds__(256)
-qb_rotate_kernel(long long rows, int n_q_heads, int gqa, const void* __restrict__ q, int dtype, RotDev rot,
-                 float* __restrict__ out) {
-  __shared__ float s_x[8][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long r = (long long)blockIdx.x * 8 + warp;
-  if (r >= rows) return;
-  const int h = (int)(r % n_q_heads) / gqa;
+__device__ __forceinline__ void qb_rotate_row(const QbArgs& a, long long r, const void* __restrict__ q, int dtype,
+                                              const RotDev& rot, float* s_x, int lane) {
+  const int h = (int)(r % a.n_q_heads) / a.gqa;
   const float4 x = load4(q, (size_t)r * D + 4 * lane, dtype);
   float y[4] = {x.x, x.y, x.z, x.w};
   if (rot.kind == KVQ_ROT_SIGNED_HADAMARD) {
@@ -118,88 +312,844 @@ qb_rotate_kernel(long long rows, int n_q_heads, int gqa, const void* __restrict_
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] *= 0.08838834764831845f;
   } else if (rot.kind == KVQ_ROT_DENSE) {
-    *reinterpret_cast<float4*>(&s_x[warp][4 * lane]) = x;
+    *reinterpret_cast<float4*>(s_x + 4 * lane) = x;
     __syncwarp();
     y[0] = y[1] = y[2] = y[3] = 0.f;
     const float* R = rot.dense + (size_t)h * D * D;
 #pragma unroll 8
     for (int c = 0; c < D; ++c) {
       const float4 w = __ldg(reinterpret_cast<const float4*>(R + c * D + 4 * lane));
-      const float v = s_x[warp][c];
+      const float v = s_x[c];
       y[0] = fmaf(v, w.x, y[0]); y[1] = fmaf(v, w.y, y[1]); y[2] = fmaf(v, w.z, y[2]); y[3] = fmaf(v, w.w, y[3]);
     }
   }
-  *reinterpret_cast<float4*>(out + (size_t)r * D + 4 * lane) =
+  *reinterpret_cast<float4*>(a.ws.q + (size_t)r * D + 4 * lane) =
       make_float4(y[0] * QB_SCALE, y[1] * QB_SCALE, y[2] * QB_SCALE, y[3] * QB_SCALE);
 }
 
-__global__ void __launch_bounds__(256)
-qb_attend_kernel(PageGeom g, int n_q_heads, int gqa, int n_seqs, int n_total, int max_q, int max_len, int mode,
-                 const int32_t* __restrict__ cu_q, const int32_t* __restrict__ lens,
-                 const int32_t* __restrict__ table, const uint8_t* __restrict__ pool, QbWs ws, float* __restrict__ out,
-                 unsigned* err) {
-  const int lane = threadIdx.x & 31;
-  const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(r / n_q_heads), j = (int)(r % n_q_heads), h = j / gqa;
-  if (t >= n_total || t >= cu_q[n_seqs]) return;
-  int lo = 0, hi = n_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu_q[mid] <= t) lo = mid;
-    else hi = mid;
+template <int N>
+__global__ void __launch_bounds__(QB_PREP_THREADS)
+qb_prepare_kernel(QbArgs a, const int32_t* __restrict__ parents, const void* __restrict__ q, int dtype, RotDev rot) {
+  __shared__ __align__(16) float s_x[QB_PREP_THREADS / 32][D];
+  pdl_launch_dependents();
+  const int trees = a.mode == QB_TREE ? a.n_seqs : 0;
+  if (blockIdx.x == 0) {
+    qb_list_tiles<N>(a);
+  } else if ((int)blockIdx.x <= trees) {
+    qb_number_tree(a, blockIdx.x - 1, parents);
+  } else {
+    const long long r = (long long)(blockIdx.x - 1 - trees) * (QB_PREP_THREADS / 32) + (threadIdx.x >> 5);
+    if (r < (long long)a.n_total * a.n_q_heads)
+      qb_rotate_row(a, r, q, dtype, rot, s_x[threadIdx.x >> 5], threadIdx.x & 31);
   }
-  const QbSeq q = qb_seq(lo, cu_q, lens, n_total, max_q, max_len, mode, err);
-  if (t < q.c0 || t >= q.c0 + q.n) return;
-  const int i = t - q.c0, base = mode == QB_CROSS ? q.len : q.len - q.n;
-  const int tin = mode == QB_TREE ? ws.tree[t].x : i;
-  const float4 y = *reinterpret_cast<const float4*>(ws.q + (size_t)r * D + 4 * lane);
-  const int P = g.page_tokens;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < q.len; ++s) {
-    if (s >= base) {
-      const int a = s - base;
-      const int2 ta = mode == QB_TREE ? ws.tree[q.c0 + a] : make_int2(a, q.n - a);
-      if ((unsigned)(tin - ta.x) >= (unsigned)ta.y) continue;
-    }
-    const int page = table[(size_t)lo * g.max_blocks + s / P], slot = s % P;
-    if ((unsigned)page >= (unsigned)g.num_blocks) {
-      flag_error(err, ERR_BLOCK_RANGE);
-      continue;
-    }
-    const uint8_t* rec = pool + ((size_t)page * g.n_kv_heads + h) * g.record;
-    const unsigned kc = rec[32 * slot + lane], vc = rec[32 * (P + slot) + lane];
-    const float2 km = __half22float2(*reinterpret_cast<const __half2*>(rec + 64 * P + 4 * slot));
-    const float2 vm = __half22float2(*reinterpret_cast<const __half2*>(rec + 68 * P + 4 * slot));
-    float a = y.x * fmaf(km.x, (float)(kc & 3), km.y);
-    a = fmaf(y.y, fmaf(km.x, (float)((kc >> 2) & 3), km.y), a);
-    a = fmaf(y.z, fmaf(km.x, (float)((kc >> 4) & 3), km.y), a);
-    a = fmaf(y.w, fmaf(km.x, (float)(kc >> 6), km.y), a);
+}
+
+// ---------------------------------------------------------------------------
+// Tensor memory wrappers of this kernel
+// ---------------------------------------------------------------------------
+// D[tmem] (+)= A[tmem] B[smem]^T, fp16 operands, by one thread.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+// fp16 A and B, fp32 D, M = 128; B K-major or (rows of N) MN-major (bit 16).
+__host__ __device__ constexpr uint32_t qb_idesc(int n, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+#define QB_R8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// this thread's lane, 32 consecutive columns
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      QB_R8(r, 0), QB_R8(r, 8), QB_R8(r, 16), QB_R8(r, 24)
+      : "memory");
+}
+// 16 lanes x 64 columns: thread t holds row t / 4 (and + 8), column t % 4 of every group of four columns
+__device__ __forceinline__ void tmem_st16x128_x16(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      QB_R8(r, 0), QB_R8(r, 8), QB_R8(r, 16), QB_R8(r, 24)
+      : "memory");
+}
+#undef QB_R8
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 consecutive columns of this thread's lane; the load and its wait are one statement.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 #pragma unroll
-    for (int d = 16; d; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
-    const float mn = fmaxf(m, a);
-    const float f = exp2f(m - mn), p = exp2f(a - mn);
-    m = mn;
-    l = fmaf(l, f, p);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+template <int C>
+__device__ __forceinline__ void qb_tmem_ld(uint32_t taddr, float (&v)[C]) {
+  static_assert(C == 8 || C == 16, "columns");
+  if constexpr (C == 8) tmem_ld8(taddr, v);
+  else tmem_ld16(taddr, v);
+}
+
+// ---------------------------------------------------------------------------
+// Expansion of 2-bit codes: field F (bits 2F, 2F + 1) of both 16-bit halves of x as
+// the fp16 pair c - 1.5.  The field lands in the mantissa of 2^k + c (exact), from
+// which 2^k + 1.5 is subtracted (exact); fields that straddle the exponent bits are
+// taken from the byte-swapped halves.
+// ---------------------------------------------------------------------------
+template <int F>
+__device__ __forceinline__ uint32_t qb_field(uint32_t x, uint32_t x_swapped) {
+  constexpr int bit = F == 0 ? 8 : F <= 4 ? 2 * F : 2 * F - 8;  // 2, 4, 6 or 8
+  constexpr bool swapped = F == 0 || F >= 5;
+  constexpr uint32_t mask = 0x00030003u << bit;
+  constexpr uint32_t e = (uint32_t)(25 - bit) << 10;            // 2^(10 - bit): one unit of c at that bit
+  constexpr uint32_t magic = e | (e << 16);
+  // 2^k + 1.5: mantissa 1.5 * 2^bit
+  constexpr uint32_t off16 = e + (3u << (bit - 1)), off = off16 | (off16 << 16);
+  const uint32_t v = ((swapped ? x_swapped : x) & mask) | magic;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), __halves2half2(__ushort_as_half(off & 0xffff), __ushort_as_half(off & 0xffff)));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t qb_swap(uint32_t x) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %1, 0x2301;" : "=r"(d) : "r"(x));
+  return d;
+}
+
+// Values: one field of 32 transposed registers into 16 lanes of tensor memory.
+template <int F>
+__device__ __forceinline__ void qb_expand_value_field(const uint32_t (&raw)[32], uint32_t taddr) {
+  uint32_t r[32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) o[c] = fmaf(p, fmaf(vm.x, (float)((vc >> (2 * c)) & 3), vm.y), o[c] * f);
+  for (int i = 0; i < 32; ++i) r[i] = qb_field<F>(raw[i], (F == 0 || F >= 5) ? qb_swap(raw[i]) : 0u);
+  tmem_st16x128_x16(taddr + ((uint32_t)(16 * (F & 1)) << 16), r);
+}
+
+__device__ __forceinline__ int qb_ordered(float f) {
+  const int i = __float_as_int(f);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float qb_unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+__device__ __forceinline__ float qb_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t qb_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <int N>
+struct QbShared {  // alignas: read as 16-byte vectors
+  alignas(16) float sumq[2][N];     // per row of the unit's queries: sum(q')
+  alignas(16) int tin[2][N];
+  alignas(16) float neg_m[N];       // -M of the running unit
+  alignas(16) float scale[4][N];    // factors of the accumulated numerator for tile i (i % 4), where flagged
+  alignas(16) int moved[4][4];      // per chunk of rows: whether tile i moved a reference
+  alignas(16) int vote[2][2][4];    // per half of the softmax warps: the warps' votes, two rounds
+  alignas(16) int red[2][4][16];    // per half: a chunk's column maxima per warp
+  alignas(16) float lsum[4][N];
+  alignas(16) float zsum[4][N];
+  alignas(16) float m_out[N];
+  alignas(16) QbUnit unit[QB_UNITS];
+  float unscale[2];                 // 2^-E of the unit's queries
+  float qmax[4];
+  alignas(8) uint64_t full[QB_STAGES];
+  uint64_t empty[QB_STAGES];
+  uint64_t unit_full[QB_UNITS], unit_free[QB_UNITS];
+  uint64_t q_ready[2];
+  uint64_t k_ready[2], v_ready[2], s_done[2], s_free[2], p_ready[2], o_done[2], o_free[2];
+  uint64_t lz_ready, lz_free, last;
+  uint64_t group[3];                // meetings of the four warps of a softmax half (0, 1) and of the accumulation (2)
+  uint32_t tmem;
+  int abort;
+};
+static_assert(offsetof(QbShared<16>, neg_m) % 16 == 0 && offsetof(QbShared<16>, vote) % 16 == 0 &&
+                  offsetof(QbShared<16>, scale) % 16 == 0 && offsetof(QbShared<16>, sumq) % 16 == 0,
+              "vector reads");
+
+template <int N>
+__global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
+  constexpr int NH = N / 2;                     // rows of a softmax half
+  constexpr int CH = NH < 16 ? NH : 16;         // rows of a chunk
+  constexpr int NC = NH / CH;                   // chunks of a half
+  constexpr uint32_t T_K = 0, T_V = 128, T_S = 256, T_O = 384;  // tensor memory columns, two buffers of 64 each
+  extern __shared__ uint8_t qb_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(qb_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_q = smem;                          // [2 units][hi, lo][2 halves of 64 channels][N rows of 128 bytes]
+  uint8_t* s_p = s_q + 2 * N * 512;             // [2 tiles][hi, lo][128 tokens of 128 bytes]
+  uint8_t* s_stage = s_p + 4 * QB_PBUF;
+  __shared__ QbShared<N> sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr unsigned FULLM = 0xffffffffu;
+
+  if (tid == 0) {
+    for (int i = 0; i < QB_STAGES; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 4 + 8);
+    }
+    for (int i = 0; i < QB_UNITS; ++i) {
+      mbar_init(&sh.unit_full[i], 1);
+      mbar_init(&sh.unit_free[i], 8 + 4 + 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_ready[i], 4);
+      mbar_init(&sh.k_ready[i], 4);
+      mbar_init(&sh.v_ready[i], 4);
+      mbar_init(&sh.s_done[i], 1);
+      mbar_init(&sh.s_free[i], 8);
+      mbar_init(&sh.p_ready[i], 8);
+      mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.o_free[i], 4);
+    }
+    mbar_init(&sh.lz_ready, 8);
+    mbar_init(&sh.lz_free, 4);
+    mbar_init(&sh.last, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&sh.group[i], 4);
+    sh.abort = 0;
+    fence_mbar_init();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<float4*>(out + (size_t)r * D + 4 * lane) = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+  if (warp == 0) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long total = a.ws.tiles[a.n_seqs];
+  const long long first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
+  const int n_tiles = (int)(last - first);
+
+  auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&sh.abort) != 0; };
+  // warp-uniform bounded wait; false (and the CTA gives up) on a time-out
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = __all_sync(FULLM, mbar_wait_bounded(bar, parity & 1));
+    if (!ok && lane == 0) {
+      flag_error(a.err, ERR_TIMEOUT);
+      *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+    }
+    return ok && !aborted();
+  };
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  // the four warps of a group meet (a bounded wait, unlike a hardware barrier)
+  uint32_t round = 0;
+  auto meet = [&](int group) {
+    arrive(&sh.group[group]);
+    return wait(&sh.group[group], round++);
+  };
+
+  if (n_tiles > 0) {
+    if (warp < 4) {
+      // ---- codes -> tensor memory ----
+      const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+      const int P = a.g.page_tokens;
+      const int tok = 32 * warp + lane;
+      const int k_off = (tok / P) * a.g.record + 32 * (tok % P);
+      // rows of the transposing loads: lane l gives row l % 8 of matrix l / 8
+      const int vt = (lane & 7) + ((lane >> 4) << 3), vh = (lane >> 3) & 1;
+      for (int i = 0; i < n_tiles; ++i) {
+        const int st = i % QB_STAGES, buf = i & 1, use = i >> 1;
+        const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
+        if (!wait(&sh.full[st], i / QB_STAGES)) break;
+        uint4 kw[2];
+        kw[0] = *reinterpret_cast<const uint4*>(stage + k_off);
+        kw[1] = *reinterpret_cast<const uint4*>(stage + k_off + 16);
+        if (use && !wait(&sh.s_done[buf], use - 1)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t w[4] = {kw[half].x, kw[half].y, kw[half].z, kw[half].w};
+          uint32_t r[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t x = w[j], y = qb_swap(w[j]);
+            r[8 * j + 0] = qb_field<0>(x, y);
+            r[8 * j + 1] = qb_field<1>(x, y);
+            r[8 * j + 2] = qb_field<2>(x, y);
+            r[8 * j + 3] = qb_field<3>(x, y);
+            r[8 * j + 4] = qb_field<4>(x, y);
+            r[8 * j + 5] = qb_field<5>(x, y);
+            r[8 * j + 6] = qb_field<6>(x, y);
+            r[8 * j + 7] = qb_field<7>(x, y);
+          }
+          tmem_st32(tmem + lanes + T_K + 64 * buf + 32 * half, r);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&sh.k_ready[buf]);
+        uint32_t raw[32];
+#pragma unroll
+        for (int g16 = 0; g16 < 8; ++g16) {
+          const int t = 16 * g16 + vt;
+          uint32_t r4[4];
+          ldsm_x4_trans(smem_u32(stage + (t / P) * a.g.record + 32 * P + 32 * (t % P) + 16 * vh), r4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) raw[4 * g16 + j] = r4[j];
+        }
+        arrive(&sh.empty[st]);
+        if (use && !wait(&sh.o_done[buf], use - 1)) break;
+        tc_fence_after();
+        const uint32_t ta = tmem + lanes + T_V + 64 * buf;
+        if (warp == 0) {
+          qb_expand_value_field<0>(raw, ta);
+          qb_expand_value_field<1>(raw, ta);
+        } else if (warp == 1) {
+          qb_expand_value_field<2>(raw, ta);
+          qb_expand_value_field<3>(raw, ta);
+        } else if (warp == 2) {
+          qb_expand_value_field<4>(raw, ta);
+          qb_expand_value_field<5>(raw, ta);
+        } else {
+          qb_expand_value_field<6>(raw, ta);
+          qb_expand_value_field<7>(raw, ta);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&sh.v_ready[buf]);
+      }
+    } else if (warp < 12) {
+      // ---- softmax: one token a thread, rows col0 .. col0 + NH - 1 ----
+      const int half = (warp - 4) >> 2, q4 = warp & 3, col0 = half * NH;
+      const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+      const int P = a.g.page_tokens, tok = 32 * q4 + lane;
+      const int meta_off = (tok / P) * a.g.record + 64 * P + 4 * (tok % P);
+      const bool lead = tid == 128 + 128 * half;
+      int i = 0;
+      bool ok = true;
+      for (int un = 0; ok; ++un) {
+        if (!wait(&sh.unit_full[un % QB_UNITS], un / QB_UNITS)) break;
+        const QbUnit u = sh.unit[un % QB_UNITS];
+        arrive(&sh.unit_free[un % QB_UNITS]);
+        if (u.t1 == u.t0) break;
+        if (!wait(&sh.q_ready[un & 1], un >> 1)) break;
+        const float unscale = sh.unscale[un & 1];
+        const float* s_sumq = sh.sumq[un & 1];
+        const int* s_tin = sh.tin[un & 1];
+        const int base = a.mode == QB_CROSS ? u.len : u.len - u.n;
+        // positions below `open` are seen by every row of the tile
+        const int open = a.mode == QB_CHAIN ? base + u.rt * (N / a.gqa) + 1 : base;
+        if (!meet(half)) break;  // the last unit's references are no longer read
+        if (tok < NH) sh.neg_m[col0 + tok] = -QB_NONE;
+        if (!meet(half)) break;
+        uint64_t l2[NH / 2], z2[NH / 2];
+#pragma unroll
+        for (int j = 0; j < NH / 2; ++j) l2[j] = z2[j] = 0ull;
+        for (int t = u.t0; t < u.t1; ++t, ++i) {
+          const int st = i % QB_STAGES, buf = i & 1, use = i >> 1;
+          const uint8_t* meta = s_stage + st * QB_STAGE_BYTES + meta_off;
+          if (!(ok = wait(&sh.full[st], i / QB_STAGES))) break;
+          const float2 km = __half22float2(*reinterpret_cast<const __half2*>(meta));
+          const float2 vm = __half22float2(*reinterpret_cast<const __half2*>(meta + 4 * P));
+          arrive(&sh.empty[st]);
+          const int pos = t * QB_TOK + tok;
+          const bool masked = (t + 1) * QB_TOK > open;
+          int key_tin = 0;
+          unsigned key_size = 0x7fffffffu;
+          if (masked) {
+            if (pos >= u.len) {
+              key_size = 0u;
+            } else if (pos >= base) {
+              const int d = pos - base;
+              const int2 ts = a.mode == QB_TREE ? a.ws.tree[u.c0 + d] : make_int2(d, u.n - d);
+              key_tin = ts.x;
+              key_size = (unsigned)ts.y;
+            }
+          }
+          const float sv = vm.x == 0.f ? 5.9604644775390625e-08f : vm.x;
+          const float ls = __log2f(sv), inv = __frcp_rn(sv);
+          const float sk = km.x * unscale, kmid = fmaf(1.5f, km.x, km.y), zc = inv * fmaf(1.5f, sv, vm.y);
+          const uint64_t sk2 = f2pk(sk, sk), kmid2 = f2pk(kmid, kmid), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
+                         zc2 = f2pk(zc, zc);
+          if (!(ok = wait(&sh.s_done[buf], use))) break;
+          tc_fence_after();
+          uint8_t* p_hi = s_p + (2 * buf) * QB_PBUF + tok * 128;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const int col = col0 + c * CH;
+            float x[CH];
+            qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col, x);
+            uint32_t see = 0xffffffffu;
+            if (masked) {
+              see = 0u;
+#pragma unroll
+              for (int j = 0; j < CH; ++j) see |= ((unsigned)(s_tin[col + j] - key_tin) < key_size ? 1u : 0u) << j;
+            }
+            float top = -INFINITY;
+            auto logits = [&](bool raw) {  // x: a + log2 s - M (raw: without M)
+#pragma unroll
+              for (int j = 0; j < CH; j += 4) {
+                const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col + j);
+                float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + col + j);
+                if (raw) nm = make_float4(0.f, 0.f, 0.f, 0.f);
+                const uint64_t u0 = f2fma(kmid2, f2pk(sq.x, sq.y), f2add(f2pk(nm.x, nm.y), ls2));
+                const uint64_t u1 = f2fma(kmid2, f2pk(sq.z, sq.w), f2add(f2pk(nm.z, nm.w), ls2));
+                const float2 d0 = f2up(f2fma(sk2, f2pk(x[j], x[j + 1]), u0));
+                const float2 d1 = f2up(f2fma(sk2, f2pk(x[j + 2], x[j + 3]), u1));
+                x[j] = d0.x; x[j + 1] = d0.y; x[j + 2] = d1.x; x[j + 3] = d1.y;
+              }
+              if (masked) {
+#pragma unroll
+                for (int j = 0; j < CH; ++j) x[j] = (see >> j) & 1u ? x[j] : -INFINITY;
+              }
+            };
+            logits(false);
+#pragma unroll
+            for (int j = 0; j < CH; ++j) top = fmaxf(top, x[j]);
+            const bool mine = __any_sync(FULLM, top > QB_TRIGGER);
+            int* votes = sh.vote[half][round & 1];
+            if (lane == 0) votes[q4] = mine;
+            if (!(ok = meet(half))) break;
+            const int4 v4 = *reinterpret_cast<const int4*>(votes);
+            const bool move = (v4.x | v4.y | v4.z | v4.w) != 0;
+            if (lead) sh.moved[i & 3][half * NC + c] = move;
+            if (move) {
+              // the chunk's references are set anew: column maxima over the 128 tokens
+              qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col, x);
+              logits(true);
+              int col_max = 0;
+#pragma unroll
+              for (int j = 0; j < CH; ++j) {
+                const int m = __reduce_max_sync(FULLM, qb_ordered(x[j]));
+                if (lane == j) col_max = m;
+              }
+              if (lane < CH) sh.red[half][q4][lane] = col_max;
+              if (!(ok = meet(half))) break;
+              if (tok < CH) {
+                const int m = max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
+                                  max(sh.red[half][2][tok], sh.red[half][3][tok]));
+                const float old = -sh.neg_m[col + tok], now = fmaxf(old, qb_unordered(m) - QB_LIFT);
+                sh.neg_m[col + tok] = -now;
+                sh.scale[i & 3][col + tok] = qb_ex2(old - now);
+              }
+              if (!(ok = meet(half))) break;
+              qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col, x);
+              logits(false);
+#pragma unroll
+              for (int j = 0; j < CH; j += 2) {
+                const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col + j);
+                const uint64_t f2 = f2pk(f.x, f.y);
+                l2[(c * CH + j) / 2] = f2mul(l2[(c * CH + j) / 2], f2);
+                z2[(c * CH + j) / 2] = f2mul(z2[(c * CH + j) / 2], f2);
+              }
+            }
+            if (c == NC - 1) {  // the scores are in registers
+              tc_fence_before();
+              arrive(&sh.s_free[buf]);
+            }
+            if (c == 0 && use && !(ok = wait(&sh.o_done[buf], use - 1))) break;
+#pragma unroll
+            for (int j = 0; j < CH; ++j) x[j] = qb_ex2(x[j]);
+            if (!masked) {
+#pragma unroll
+              for (int j = 0; j < CH; j += 2) {
+                const uint64_t w2 = f2pk(x[j], x[j + 1]);
+                l2[(c * CH + j) / 2] = f2fma(w2, inv2, l2[(c * CH + j) / 2]);
+                z2[(c * CH + j) / 2] = f2fma(w2, zc2, z2[(c * CH + j) / 2]);
+              }
+            } else {  // an unseen token adds exactly nothing, whatever its scale and zero are
+#pragma unroll
+              for (int j = 0; j < CH; j += 2) {
+                const bool v0 = (see >> j) & 1u, v1 = (see >> (j + 1)) & 1u;
+                l2[(c * CH + j) / 2] = f2add(l2[(c * CH + j) / 2], f2pk(v0 ? x[j] * inv : 0.f, v1 ? x[j + 1] * inv : 0.f));
+                z2[(c * CH + j) / 2] = f2add(z2[(c * CH + j) / 2], f2pk(v0 ? x[j] * zc : 0.f, v1 ? x[j + 1] * zc : 0.f));
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < CH; j += 8) {
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float w0 = x[j + 2 * k], w1 = x[j + 2 * k + 1];
+                hi[k] = qb_half2(w0, w1);
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+                lo[k] = qb_half2(w0 - back.x, w1 - back.y);
+              }
+              const int at = (((col + j) >> 3) ^ (tok & 7)) << 4;
+              *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(p_hi + QB_PBUF + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+          }
+          if (!ok) break;
+          fence_proxy_async();
+          arrive(&sh.p_ready[buf]);
+        }
+        if (!ok) break;
+        // the unit's l and sum p mid: over the warp's 32 tokens by exchange and halving, over the warps by the writer
+        float l[NH], z[NH];
+#pragma unroll
+        for (int j = 0; j < NH / 2; ++j) {
+          const float2 p = f2up(l2[j]), q = f2up(z2[j]);
+          l[2 * j] = p.x; l[2 * j + 1] = p.y;
+          z[2 * j] = q.x; z[2 * j + 1] = q.y;
+        }
+        int cols = 0;  // column this lane ends up with
+        int width = NH;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) {
+          if (d >= 32 / NH * 1 && width > 1) {
+            width >>= 1;
+            const bool up = lane & d;
+#pragma unroll
+            for (int j = 0; j < NH / 2; ++j) {
+              if (j < width) {
+                const float sl = up ? l[j] : l[j + width], sz = up ? z[j] : z[j + width];
+                const float kl = up ? l[j + width] : l[j], kz = up ? z[j + width] : z[j];
+                l[j] = kl + __shfl_xor_sync(FULLM, sl, d);
+                z[j] = kz + __shfl_xor_sync(FULLM, sz, d);
+              }
+            }
+            if (up) cols += width;
+          } else {
+            l[0] += __shfl_xor_sync(FULLM, l[0], d);
+            z[0] += __shfl_xor_sync(FULLM, z[0], d);
+          }
+        }
+        if (un && !wait(&sh.lz_free, un - 1)) break;
+        if ((lane & (32 / NH - 1)) == 0) {
+          sh.lsum[q4][col0 + cols] = l[0];
+          sh.zsum[q4][col0 + cols] = z[0];
+        }
+        if (tok < NH) sh.m_out[col0 + tok] = -sh.neg_m[col0 + tok];
+        arrive(&sh.lz_ready);
+      }
+    } else if (warp < 16) {
+      // ---- accumulation: one channel a thread ----
+      const int q4 = warp & 3, wt = tid - 384;
+      const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+      const int ch = 8 * (lane & 15) + 2 * q4 + (lane >> 4);
+      constexpr int TPR = 128 / N;  // threads a query row
+      const int row = wt / TPR, part = wt % TPR;
+      // queries of unit `un` into its buffer, with their sums and the tile's exponent
+      auto load_queries = [&](int un, const QbUnit& u) {
+        const int R = u.rt * N + row, tk = R / a.gqa;
+        const bool valid = tk < u.n;
+        const float* src = a.ws.q + ((size_t)(u.c0 + (valid ? tk : 0)) * a.n_q_heads + u.h * a.gqa + R % a.gqa) * D + part * N;
+        float m = 0.f, s = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < N; j += 4) {
+          const float4 v = valid ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+          s += (v.x + v.y) + (v.z + v.w);
+          const float w[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m = w[k] <= 3.0e38f ? fmaxf(m, w[k]) : m;  // of the finite ones
+        }
+#pragma unroll
+        for (int d = 1; d < TPR; d <<= 1) s += __shfl_xor_sync(FULLM, s, d);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(FULLM, m, d));
+        if (lane == 0) sh.qmax[q4] = m;
+        if (!meet(2)) return false;
+        m = fmaxf(fmaxf(sh.qmax[0], sh.qmax[1]), fmaxf(sh.qmax[2], sh.qmax[3]));
+        // the largest at 2^13 .. 2^14
+        const int e = m > 0.f ? min(100, max(-100, 13 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
+        const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
+        uint8_t* dst = s_q + (un & 1) * N * 512 + row * 128;
+#pragma unroll
+        for (int j = 0; j < N; j += 16) {
+          float v[16];
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            const float4 x = valid ? *reinterpret_cast<const float4*>(src + j + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[k] = x.x * scale; v[k + 1] = x.y * scale; v[k + 2] = x.z * scale; v[k + 3] = x.w * scale;
+          }
+          // K order of the expanded keys: channels f and 8 + f of a 16-channel word side by side
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int f = 0; f < 8; ++f) {
+            hi[f] = qb_half2(v[f], v[8 + f]);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[f]));
+            lo[f] = qb_half2(v[f] - back.x, v[8 + f] - back.y);
+          }
+          const int w = (part * N + j) >> 4;  // 16-channel word
+          uint8_t* d = dst + (w >> 2) * N * 128;
+          const int c0 = ((2 * (w & 3)) ^ (row & 7)) << 4, c1 = ((2 * (w & 3) + 1) ^ (row & 7)) << 4;
+          *reinterpret_cast<uint4*>(d + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(d + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+          *reinterpret_cast<uint4*>(d + N * 256 + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(d + N * 256 + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+        }
+        if (part == 0) {
+          sh.sumq[un & 1][row] = s;
+          sh.tin[un & 1][row] = !valid ? 0 : a.mode == QB_TREE ? a.ws.tree[u.c0 + tk].x : a.mode == QB_CHAIN ? tk : 0;
+        }
+        if (wt == 0) sh.unscale[un & 1] = __uint_as_float((uint32_t)(127 - e) << 23);
+        fence_proxy_async();
+        arrive(&sh.q_ready[un & 1]);
+        return meet(2);  // qmax may be written again
+      };
+      bool ok = wait(&sh.unit_full[0], 0);
+      QbUnit u = sh.unit[0];
+      if (ok) ok = load_queries(0, u);
+      int i = 0;
+      for (int un = 0; ok; ++un) {
+        if (!(ok = wait(&sh.unit_full[(un + 1) % QB_UNITS], (un + 1) / QB_UNITS))) break;
+        const QbUnit next = sh.unit[(un + 1) % QB_UNITS];
+        arrive(&sh.unit_free[un % QB_UNITS]);
+        if (next.t1 > next.t0 && !(ok = load_queries(un + 1, next))) break;
+        float acc[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) acc[j] = 0.f;
+        for (int t = u.t0; t < u.t1; ++t, ++i) {
+          const int buf = i & 1, use = i >> 1;
+          if (!(ok = wait(&sh.o_done[buf], use))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < N / CH; ++c) {
+            float o[CH];
+            qb_tmem_ld<CH>(tmem + lanes + T_O + 64 * buf + c * CH, o);
+            if (sh.moved[i & 3][c]) {
+#pragma unroll
+              for (int j = 0; j < CH; ++j) acc[c * CH + j] = fmaf(acc[c * CH + j], sh.scale[i & 3][c * CH + j], o[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < CH; j += 2) {
+                const float2 s = f2up(f2add(f2pk(acc[c * CH + j], acc[c * CH + j + 1]), f2pk(o[j], o[j + 1])));
+                acc[c * CH + j] = s.x;
+                acc[c * CH + j + 1] = s.y;
+              }
+            }
+          }
+          tc_fence_before();
+          arrive(&sh.o_free[buf]);
+        }
+        if (!ok || !(ok = wait(&sh.lz_ready, un))) break;
+        const bool whole = u.t0 == 0 && u.t1 == u.nt;
+        float* part_base = a.ws.part + (size_t)(2 * blockIdx.x + (u.t0 == 0 ? 1 : 0)) * N * (D + 2);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float l = (sh.lsum[0][j] + sh.lsum[1][j]) + (sh.lsum[2][j] + sh.lsum[3][j]);
+          const float z = (sh.zsum[0][j] + sh.zsum[1][j]) + (sh.zsum[2][j] + sh.zsum[3][j]);
+          const float o = acc[j] + z;
+          if (whole) {
+            const int R = u.rt * N + j, tk = R / a.gqa;
+            if (tk < u.n)
+              a.out[((size_t)(u.c0 + tk) * a.n_q_heads + u.h * a.gqa + R % a.gqa) * D + ch] = l != 0.f ? o / l : 0.f;
+          } else {
+            part_base[j * D + ch] = o;
+            if (wt == j) {
+              part_base[N * D + j] = l;
+              part_base[N * D + N + j] = sh.m_out[j];
+            }
+          }
+        }
+        arrive(&sh.lz_free);
+        if (next.t1 == next.t0) {
+          arrive(&sh.unit_free[(un + 1) % QB_UNITS]);
+          break;
+        }
+        u = next;
+      }
+    } else if (warp == 16) {
+      // ---- page copies, and the list of units one ahead of them ----
+      QbUnit u = qb_locate<N>(a, first, lane), ahead;
+      long long left = n_tiles;
+      auto publish = [&](int un, QbUnit v, long long room) {
+        if (room <= 0) v.t0 = v.t1 = 0;
+        else if (v.t1 - v.t0 > room) v.t1 = v.t0 + (int)room;
+        bool ok = true;
+        if (un >= QB_UNITS) ok = wait(&sh.unit_free[un % QB_UNITS], un / QB_UNITS - 1);
+        if (lane == 0) sh.unit[un % QB_UNITS] = v;
+        arrive(&sh.unit_full[un % QB_UNITS]);
+        return ok;
+      };
+      bool ok = publish(0, u, left);
+      const int pages = QB_TOK / a.g.page_tokens;
+      int i = 0;
+      for (int un = 0; ok && left > 0; ++un) {
+        if (u.t1 - u.t0 > left) u.t1 = u.t0 + (int)left;
+        left -= u.t1 - u.t0;
+        ahead = u;
+        if (left > 0) qb_next<N>(a, ahead);
+        if (!(ok = publish(un + 1, ahead, left))) break;
+        const int32_t* row = a.table + (size_t)u.b * a.g.max_blocks;
+        auto page_of = [&](int t) {  // this lane's page of tile t, -1 where there is none
+          const int p = t * pages + lane;
+          return t < u.t1 && lane < pages && (long long)p * a.g.page_tokens < u.len ? row[p] : -1;
+        };
+        auto expected = [&](int t) { return lane < pages && (long long)(t * pages + lane) * a.g.page_tokens < u.len; };
+        int id = page_of(u.t0);
+        for (int t = u.t0; t < u.t1; ++t, ++i) {
+          const int st = i % QB_STAGES;
+          const int id_next = page_of(t + 1);
+          const bool want = expected(t), good = want && (unsigned)id < (unsigned)a.g.num_blocks;
+          if (want && !good) flag_error(a.err, ERR_BLOCK_RANGE);
+          if (i >= QB_STAGES && !(ok = wait(&sh.empty[st], i / QB_STAGES - 1))) break;
+          const int n = __popc(__ballot_sync(FULLM, good));
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[st], n * a.g.record);
+          __syncwarp();
+          if (good)
+            bulk_g2s(s_stage + st * QB_STAGE_BYTES + lane * a.g.record,
+                     a.pool + ((size_t)id * a.g.n_kv_heads + u.h) * a.g.record, a.g.record, &sh.full[st]);
+          id = id_next;
+        }
+        u = ahead;
+      }
+      if (!ok)  // no copy in flight when the CTA ends
+        for (int k = max(0, i - QB_STAGES); k < i; ++k) mbar_wait_bounded(&sh.full[k % QB_STAGES], (k / QB_STAGES) & 1);
+    } else {
+      // ---- MMA issue ----
+      constexpr uint32_t I_QK = qb_idesc(N, false), I_PV = qb_idesc(N, true);
+      auto pv = [&](int i) {
+        const int buf = i & 1, use = i >> 1;
+        if (!wait(&sh.v_ready[buf], use) || !wait(&sh.p_ready[buf], use) || (use && !wait(&sh.o_free[buf], use - 1)))
+          return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t hi = sw128_desc(s_p + (2 * buf) * QB_PBUF), lo = sw128_desc(s_p + (2 * buf + 1) * QB_PBUF);
+          const uint32_t av = tmem + T_V + 64 * buf, d = tmem + T_O + 64 * buf;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, av + 8 * k, lo + k * (2048 >> 4), I_PV, k > 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, av + 8 * k, hi + k * (2048 >> 4), I_PV, true);
+          tc_commit(&sh.o_done[buf]);
+        }
+        __syncwarp();
+        return true;
+      };
+      int i = 0;
+      bool ok = true;
+      for (int un = 0; ok; ++un) {
+        if (!(ok = wait(&sh.unit_full[un % QB_UNITS], un / QB_UNITS))) break;
+        const int count = sh.unit[un % QB_UNITS].t1 - sh.unit[un % QB_UNITS].t0;
+        arrive(&sh.unit_free[un % QB_UNITS]);
+        if (count == 0) break;
+        if (!(ok = wait(&sh.q_ready[un & 1], un >> 1))) break;
+        const uint8_t* qt = s_q + (un & 1) * N * 512;
+        for (int t = 0; t < count; ++t, ++i) {
+          const int buf = i & 1, use = i >> 1;
+          if (!(ok = wait(&sh.k_ready[buf], use) && (!use || wait(&sh.s_free[buf], use - 1)))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t ak = tmem + T_K + 64 * buf, d = tmem + T_S + 64 * buf;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma_f16_ts(d, ak + 8 * k, sw128_desc(qt + (2 + (k >> 2)) * N * 128) + (k & 3) * 2, I_QK, k > 0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma_f16_ts(d, ak + 8 * k, sw128_desc(qt + (k >> 2) * N * 128) + (k & 3) * 2, I_QK, true);
+            tc_commit(&sh.s_done[buf]);
+          }
+          __syncwarp();
+          if (i > 0 && !(ok = pv(i - 1))) break;
+        }
+      }
+      if (ok) ok = pv(i - 1);
+      if (!ok) {  // let the tensor cores finish before their memory is freed
+        if (lane == 0) tc_commit(&sh.last);
+        __syncwarp();
+        mbar_wait_bounded(&sh.last, 0);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Units cut by slices.  Block k joins the unit that starts in slice k and runs past its
+// end: its partial there (slot 2k + 1) and slots 2j of the following slices, in order.
+constexpr int QB_JOIN_ROWS = 8;
+
+template <int N>
+__global__ void __launch_bounds__(D) qb_combine_kernel(QbArgs a, int grid) {
+  __shared__ QbUnit s_u;
+  __shared__ long long s_u0;
+  pdl_wait();
+  const long long total = a.ws.tiles[a.n_seqs];
+  const int k = blockIdx.x;
+  const long long start = total * k / grid, end = total * (k + 1) / grid;
+  if (end == start) return;
+  if (threadIdx.x < 32) {
+    const QbUnit u = qb_locate<N>(a, end - 1, threadIdx.x);
+    if (threadIdx.x == 0) {
+      s_u = u;
+      s_u0 = end - 1 - u.t0;
+    }
+  }
+  __syncthreads();
+  const QbUnit u = s_u;
+  const long long u0 = s_u0, u1 = u0 + u.nt;
+  if (u1 <= end || u0 < start) return;
+  int j1 = k + 1;  // the slice after the last one that holds a part (an empty slice holds none)
+  while (j1 < grid && total * j1 / grid < u1) ++j1;
+  for (int r = blockIdx.y * QB_JOIN_ROWS; r < (int)(blockIdx.y + 1) * QB_JOIN_ROWS; ++r) {
+    const int R = u.rt * N + r, tk = R / a.gqa;
+    if (tk >= u.n) return;
+    float m = QB_NONE;
+    for (int j = k; j < j1; ++j) {
+      if (total * j / grid == total * (j + 1) / grid) continue;
+      m = fmaxf(m, a.ws.part[(size_t)(2 * j + (j == k)) * N * (D + 2) + N * D + N + r]);
+    }
+    float o = 0.f, l = 0.f;
+    for (int j = k; j < j1; ++j) {
+      if (total * j / grid == total * (j + 1) / grid) continue;
+      const float* p = a.ws.part + (size_t)(2 * j + (j == k)) * N * (D + 2);
+      const float f = exp2f(p[N * D + N + r] - m);
+      o = fmaf(p[r * D + threadIdx.x], f, o);
+      l = fmaf(p[N * D + r], f, l);
+    }
+    a.out[((size_t)(u.c0 + tk) * a.n_q_heads + u.h * a.gqa + R % a.gqa) * D + threadIdx.x] = l != 0.f ? o / l : 0.f;
+  }
+}
+
+template <typename K, typename... A>
+static cudaError_t qb_launch_pdl(K kernel, dim3 grid, int block, int smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int N>
+static cudaError_t qb_launch(const QbArgs& a, const int32_t* parents, const void* q, int dtype, RotDev rot, int grid,
+                             cudaStream_t s) {
+  static std::atomic<unsigned long long> attr{0};  // per device
+  cudaError_t e = smem_limit_once(attr, qb_attend_kernel<N>, qb_smem_bytes(N));
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)a.n_total * a.n_q_heads;
+  const long long blocks = 1 + (a.mode == QB_TREE ? a.n_seqs : 0) + (rows + QB_PREP_THREADS / 32 - 1) / (QB_PREP_THREADS / 32);
+  qb_prepare_kernel<N><<<(unsigned)blocks, QB_PREP_THREADS, 0, s>>>(a, parents, q, dtype, rot);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = qb_launch_pdl(qb_attend_kernel<N>, dim3(grid), QB_THREADS, qb_smem_bytes(N), s, a)) != cudaSuccess) return e;
+  return qb_launch_pdl(qb_combine_kernel<N>, dim3(grid, N / QB_JOIN_ROWS), D, 0, s, a, grid);
 }
 
 cudaError_t launch_query_block(const PageGeom& g, int n_q_heads, int n_seqs, int n_total, const void* q, int dtype,
                                const int32_t* cu_q, int max_q, const int32_t* parents, int mode, const int32_t* lens,
                                int max_len, const int32_t* table, RotDev rot_k, const uint8_t* pool, void* ws_base,
                                float* o_rot, unsigned* err, cudaStream_t s) {
-  QbWs ws;
-  qb_layout(ws_base, n_total, n_q_heads, &ws);
-  const int gqa = n_q_heads / g.n_kv_heads;
-  const long long rows = (long long)n_total * n_q_heads;
-  if (mode == QB_TREE) qb_tree_kernel<<<n_seqs, 256, 0, s>>>(cu_q, lens, parents, n_total, max_q, max_len, ws.tree, err);
-  qb_rotate_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(rows, n_q_heads, gqa, q, dtype, rot_k, ws.q);
-  qb_attend_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(g, n_q_heads, gqa, n_seqs, n_total, max_q, max_len, mode,
-                                                              cu_q, lens, table, pool, ws, o_rot, err);
-  return cudaGetLastError();
+  const int gqa = n_q_heads / g.n_kv_heads, rows = qb_rows(max_q, gqa), grid = device_sm_count();
+  QbArgs a{g, n_q_heads, gqa, n_seqs, n_total, max_q, max_len, mode, cu_q, lens, table, pool, {}, o_rot, err};
+  qb_layout(ws_base, n_seqs, n_total, n_q_heads, rows, grid, &a.ws);
+  return rows == 16   ? qb_launch<16>(a, parents, q, dtype, rot_k, grid, s)
+         : rows == 32 ? qb_launch<32>(a, parents, q, dtype, rot_k, grid, s)
+                      : qb_launch<64>(a, parents, q, dtype, rot_k, grid, s);
 }
 
 }  // namespace kvq
