@@ -53,14 +53,13 @@ constexpr float QB_SCALE = 0.12751742902274214f;  // log2(e) / sqrt(128): base-2
 constexpr int QB_TOK = 128;                       // tokens a tile
 constexpr int QB_STAGES = 4;
 constexpr int QB_STAGE_BYTES = QB_TOK * 72;
-constexpr int QB_THREADS = 18 * 32;
+constexpr int QB_THREADS = 20 * 32;                // 18 warps work; register shares go by groups of four warps
 constexpr int QB_PBUF = QB_TOK * 128;             // one half of W^T: 128 rows of 128 bytes (64 fp16 columns)
 constexpr int QB_UNITS = 4;                       // ring of unit descriptors
 constexpr float QB_LIFT = 8.f, QB_TRIGGER = 14.f; // weights: running maximum at 2^8, moved when one would pass 2^14
-constexpr float QB_NONE = -1e30f;                 // reference of a row that has seen nothing
 
 __host__ __device__ constexpr int qb_smem_bytes(int n) {
-  return 1024 + 2 * n * 512 + 2 * 2 * QB_PBUF + QB_STAGES * QB_STAGE_BYTES;
+  return 1024 + 2 * n * 512 + 2 * 2 * QB_PBUF + QB_STAGES * QB_STAGE_BYTES + n * D * 4;
 }
 
 // ---------------------------------------------------------------------------
@@ -108,6 +107,7 @@ struct QbSeq {
 struct QbArgs {
   PageGeom g;
   int n_q_heads, gqa, n_seqs, n_total, max_q, max_len, mode;
+  int gqa_shift, page_shift;  // both are powers of two
   const int32_t* cu_q;
   const int32_t* lens;
   const int32_t* table;
@@ -154,7 +154,7 @@ struct QbSpan {
 template <int N>
 __device__ __forceinline__ QbSpan qb_span(const QbArgs& a, const QbSeq& q) {
   QbSpan s;
-  s.lc = 31 - __clz(N / a.gqa);
+  s.lc = 31 - __clz(N >> a.gqa_shift);
   s.lm = 7 - s.lc;
   s.n_rt = (int)(((long long)q.n * a.gqa + N - 1) / N);
   s.nt = q.len ? (q.len + QB_TOK - 1) / QB_TOK : 1;
@@ -162,6 +162,15 @@ __device__ __forceinline__ QbSpan qb_span(const QbArgs& a, const QbSeq& q) {
   s.x = (q.len - q.n + 127) >> s.lc;
   return s;
 }
+
+// Slice k of all tiles: [start(k), start(k + 1)), sizes equal to within one.
+struct QbSlices {
+  long long each;
+  int more;
+  __device__ __forceinline__ QbSlices(long long total, int grid)
+      : each(total / grid), more((int)(total - total / grid * grid)) {}
+  __device__ __forceinline__ long long start(int k) const { return k * each + min(k, more); }
+};
 
 struct QbUnit {
   int b, rt, h;
@@ -355,27 +364,31 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a_tmem, uint6
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
+// One lane of a converged warp, in the form from which the compiler knows that the code
+// under it runs in a single thread (its matrix operands then need no per-lane loop).
+__device__ __forceinline__ bool qb_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
 // fp16 A and B, fp32 D, M = 128; B K-major or (rows of N) MN-major (bit 16).
 __host__ __device__ constexpr uint32_t qb_idesc(int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 #define QB_R8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
-// this thread's lane, 32 consecutive columns
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// this thread's lane, 16 consecutive columns
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      QB_R8(r, 0), QB_R8(r, 8), QB_R8(r, 16), QB_R8(r, 24)
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      QB_R8(r, 0), QB_R8(r, 8)
       : "memory");
 }
-// 16 lanes x 64 columns: thread t holds row t / 4 (and + 8), column t % 4 of every group of four columns
-__device__ __forceinline__ void tmem_st16x128_x16(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      QB_R8(r, 0), QB_R8(r, 8), QB_R8(r, 16), QB_R8(r, 24)
-      : "memory");
+// 16 lanes x 16 columns: thread t holds row t / 4 (and + 8), column t % 4 of every group of four columns
+__device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), QB_R8(r, 0)
+               : "memory");
 }
 #undef QB_R8
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -425,13 +438,10 @@ __device__ __forceinline__ uint32_t qb_swap(uint32_t x) {
   return d;
 }
 
-// Values: one field of 32 transposed registers into 16 lanes of tensor memory.
-template <int F>
-__device__ __forceinline__ void qb_expand_value_field(const uint32_t (&raw)[32], uint32_t taddr) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = qb_field<F>(raw[i], (F == 0 || F >= 5) ? qb_swap(raw[i]) : 0u);
-  tmem_st16x128_x16(taddr + ((uint32_t)(16 * (F & 1)) << 16), r);
+__device__ __forceinline__ uint32_t qb_permute(uint32_t x, uint32_t order) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(d) : "r"(x), "r"(order));
+  return d;
 }
 
 __device__ __forceinline__ int qb_ordered(float f) {
@@ -449,6 +459,43 @@ __device__ __forceinline__ uint32_t qb_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// One try without a time hint: the roles hand tiles to one another every few hundred
+// nanoseconds, and a suspension with a long hint was measured to wake up microseconds late.
+__device__ __forceinline__ bool qb_try_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long qb_now() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+constexpr unsigned long long QB_WAIT_NS = 2000000000ull;
+__device__ __forceinline__ bool qb_wait_slow(uint64_t* bar, uint32_t parity) {
+  const unsigned long long t0 = qb_now();
+  do {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (qb_try_wait(bar, parity)) return true;
+  } while (qb_now() - t0 < QB_WAIT_NS);
+  return false;
+}
+
+// A token's constants: key scale, key mid, log2 of the value scale, its reciprocal, value mid over value scale.
+enum { QB_C_SK, QB_C_KMID, QB_C_LS, QB_C_INV, QB_C_ZC };
+
+// Register shares of a group of four warps (the block's total stays what it was launched with).
+template <int R, bool UP>
+__device__ __forceinline__ void qb_registers() {
+  if constexpr (UP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
 template <int N>
 struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) float sumq[2][N];     // per row of the unit's queries: sum(q')
@@ -458,12 +505,15 @@ struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) int moved[4][4];      // per chunk of rows: whether tile i moved a reference
   alignas(16) int vote[2][2][4];    // per half of the softmax warps: the warps' votes, two rounds
   alignas(16) int red[2][4][16];    // per half: a chunk's column maxima per warp
+  alignas(16) float delta[2][16];   // per half: how far a chunk's references moved
+  alignas(16) float tok[4][5][QB_TOK];  // constants of tile i (i % 4): see QB_C_*
   alignas(16) float lsum[4][N];
   alignas(16) float zsum[4][N];
   alignas(16) float m_out[N];
   alignas(16) QbUnit unit[QB_UNITS];
   float unscale[2];                 // 2^-E of the unit's queries
-  float qmax[4];
+  float qmax[2][4];
+  float row_z[N], row_f[N];         // of the unit being written out
   alignas(8) uint64_t full[QB_STAGES];
   uint64_t empty[QB_STAGES];
   uint64_t unit_full[QB_UNITS], unit_free[QB_UNITS];
@@ -472,7 +522,6 @@ struct QbShared {  // alignas: read as 16-byte vectors
   uint64_t lz_ready, lz_free, last;
   uint64_t group[3];                // meetings of the four warps of a softmax half (0, 1) and of the accumulation (2)
   uint32_t tmem;
-  int abort;
 };
 static_assert(offsetof(QbShared<16>, neg_m) % 16 == 0 && offsetof(QbShared<16>, vote) % 16 == 0 &&
                   offsetof(QbShared<16>, scale) % 16 == 0 && offsetof(QbShared<16>, sumq) % 16 == 0,
@@ -489,6 +538,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
   uint8_t* s_q = smem;                          // [2 units][hi, lo][2 halves of 64 channels][N rows of 128 bytes]
   uint8_t* s_p = s_q + 2 * N * 512;             // [2 tiles][hi, lo][128 tokens of 128 bytes]
   uint8_t* s_stage = s_p + 4 * QB_PBUF;
+  float* s_out = reinterpret_cast<float*>(s_stage + QB_STAGES * QB_STAGE_BYTES);  // [N][128] of a finished unit
   __shared__ QbShared<N> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr unsigned FULLM = 0xffffffffu;
@@ -496,7 +546,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
   if (tid == 0) {
     for (int i = 0; i < QB_STAGES; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 4 + 8);
+      mbar_init(&sh.empty[i], 4);
     }
     for (int i = 0; i < QB_UNITS; ++i) {
       mbar_init(&sh.unit_full[i], 1);
@@ -516,7 +566,6 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
     mbar_init(&sh.lz_free, 4);
     mbar_init(&sh.last, 1);
     for (int i = 0; i < 3; ++i) mbar_init(&sh.group[i], 4);
-    sh.abort = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -530,18 +579,16 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const long long total = a.ws.tiles[a.n_seqs];
-  const long long first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
-  const int n_tiles = (int)(last - first);
+  const QbSlices slices(total, gridDim.x);
+  const long long first = slices.start(blockIdx.x);
+  const int n_tiles = (int)(slices.start(blockIdx.x + 1) - first);
 
-  auto aborted = [&]() { return *reinterpret_cast<volatile int*>(&sh.abort) != 0; };
-  // warp-uniform bounded wait; false (and the CTA gives up) on a time-out
+  // warp-uniform wait, bounded in time; a role that gives up ends, and with it, in time, the others
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool ok = __all_sync(FULLM, mbar_wait_bounded(bar, parity & 1));
-    if (!ok && lane == 0) {
-      flag_error(a.err, ERR_TIMEOUT);
-      *reinterpret_cast<volatile int*>(&sh.abort) = 1;
-    }
-    return ok && !aborted();
+    if (__builtin_expect(__all_sync(FULLM, qb_try_wait(bar, parity & 1)), 1)) return true;
+    const bool ok = __all_sync(FULLM, qb_wait_slow(bar, parity & 1));
+    if (!ok && lane == 0) flag_error(a.err, ERR_TIMEOUT);
+    return ok;
   };
   auto arrive = [&](uint64_t* bar) {
     __syncwarp();
@@ -556,29 +603,55 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
 
   if (n_tiles > 0) {
     if (warp < 4) {
-      // ---- codes -> tensor memory ----
+      // ---- codes -> tensor memory, and the tokens' constants ----
+      if constexpr (N == 64) qb_registers<72, false>();
       const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-      const int P = a.g.page_tokens;
+      const int ps = a.page_shift, pm = (1 << ps) - 1;
       const int tok = 32 * warp + lane;
-      const int k_off = (tok / P) * a.g.record + 32 * (tok % P);
-      // rows of the transposing loads: lane l gives row l % 8 of matrix l / 8
+      const int k_off = (tok >> ps) * a.g.record + 32 * (tok & pm);
+      const int meta_off = (tok >> ps) * a.g.record + (64 << ps) + 4 * (tok & pm);
+      // rows of the transposing loads: lane l gives row l % 8 of matrix l / 8; 16 tokens are 1152 bytes of either page size
       const int vt = (lane & 7) + ((lane >> 4) << 3), vh = (lane >> 3) & 1;
+      const int v_off = (vt >> ps) * a.g.record + (32 << ps) + 32 * (vt & pm) + 16 * vh;
+      // this warp's value fields f = 2 warp, 2 warp + 1: byte order and shift that bring them to bits 2, 3 (see qb_field)
+      uint32_t v_order[2];
+      int v_shift[2];
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int f = 2 * warp + o;
+        v_order[o] = f == 0 || f >= 5 ? 0x2301u : 0x3210u;
+        v_shift[o] = f == 0 ? 6 : f >= 5 ? 2 * f - 10 : 2 * f - 2;
+      }
       for (int i = 0; i < n_tiles; ++i) {
         const int st = i % QB_STAGES, buf = i & 1, use = i >> 1;
         const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
         if (!wait(&sh.full[st], i / QB_STAGES)) break;
-        uint4 kw[2];
-        kw[0] = *reinterpret_cast<const uint4*>(stage + k_off);
-        kw[1] = *reinterpret_cast<const uint4*>(stage + k_off + 16);
+        {
+          const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off));
+          const float2 vm = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off + (4 << ps)));
+          const float sv = vm.x == 0.f ? 5.9604644775390625e-08f : vm.x;
+          float ls = __log2f(sv), inv = __fdividef(1.f, sv), zc = inv * fmaf(1.5f, sv, vm.y);
+          if (!(fabsf(zc) <= 3.4e38f)) {  // not finite: NaN for the rows that see the token, 0 * 0 for the others
+            ls = NAN;
+            inv = zc = 0.f;
+          }
+          float(*c)[QB_TOK] = sh.tok[i & 3];
+          c[QB_C_SK][tok] = km.x;
+          c[QB_C_KMID][tok] = fmaf(1.5f, km.x, km.y);
+          c[QB_C_LS][tok] = ls;
+          c[QB_C_INV][tok] = inv;
+          c[QB_C_ZC][tok] = zc;
+        }
         if (use && !wait(&sh.s_done[buf], use - 1)) break;
         tc_fence_after();
+        // short loops on purpose: straight-line code runs at the speed of the instruction fetch
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + k_off + 8 * k);
+          uint32_t r[16];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t w[4] = {kw[half].x, kw[half].y, kw[half].z, kw[half].w};
-          uint32_t r[32];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t x = w[j], y = qb_swap(w[j]);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t x = j ? w.y : w.x, y = qb_swap(x);
             r[8 * j + 0] = qb_field<0>(x, y);
             r[8 * j + 1] = qb_field<1>(x, y);
             r[8 * j + 2] = qb_field<2>(x, y);
@@ -588,47 +661,37 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             r[8 * j + 6] = qb_field<6>(x, y);
             r[8 * j + 7] = qb_field<7>(x, y);
           }
-          tmem_st32(tmem + lanes + T_K + 64 * buf + 32 * half, r);
+          tmem_st16(tmem + lanes + T_K + 64 * buf + 16 * k, r);
         }
         tmem_wait_st();
         tc_fence_before();
         arrive(&sh.k_ready[buf]);
-        uint32_t raw[32];
-#pragma unroll
-        for (int g16 = 0; g16 < 8; ++g16) {
-          const int t = 16 * g16 + vt;
-          uint32_t r4[4];
-          ldsm_x4_trans(smem_u32(stage + (t / P) * a.g.record + 32 * P + 32 * (t % P) + 16 * vh), r4);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) raw[4 * g16 + j] = r4[j];
-        }
-        arrive(&sh.empty[st]);
         if (use && !wait(&sh.o_done[buf], use - 1)) break;
         tc_fence_after();
-        const uint32_t ta = tmem + lanes + T_V + 64 * buf;
-        if (warp == 0) {
-          qb_expand_value_field<0>(raw, ta);
-          qb_expand_value_field<1>(raw, ta);
-        } else if (warp == 1) {
-          qb_expand_value_field<2>(raw, ta);
-          qb_expand_value_field<3>(raw, ta);
-        } else if (warp == 2) {
-          qb_expand_value_field<4>(raw, ta);
-          qb_expand_value_field<5>(raw, ta);
-        } else {
-          qb_expand_value_field<6>(raw, ta);
-          qb_expand_value_field<7>(raw, ta);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {  // 32 tokens: 16 columns
+          uint32_t raw[8], r[8];
+          ldsm_x4_trans(smem_u32(stage + v_off + 2304 * k), *reinterpret_cast<uint32_t(*)[4]>(raw));
+          ldsm_x4_trans(smem_u32(stage + v_off + 2304 * k + 1152), *reinterpret_cast<uint32_t(*)[4]>(raw + 4));
+          const uint32_t ta = tmem + lanes + T_V + 64 * buf + 16 * k;
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = qb_field<1>(qb_permute(raw[j], v_order[o]) >> v_shift[o], 0u);
+            tmem_st16x128_x4(ta + ((uint32_t)(16 * o) << 16), r);
+          }
         }
+        arrive(&sh.empty[st]);
         tmem_wait_st();
         tc_fence_before();
         arrive(&sh.v_ready[buf]);
       }
     } else if (warp < 12) {
       // ---- softmax: one token a thread, rows col0 .. col0 + NH - 1 ----
+      if constexpr (N == 64) qb_registers<128, true>();
       const int half = (warp - 4) >> 2, q4 = warp & 3, col0 = half * NH;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-      const int P = a.g.page_tokens, tok = 32 * q4 + lane;
-      const int meta_off = (tok / P) * a.g.record + 64 * P + 4 * (tok % P);
+      const int tok = 32 * q4 + lane;
       const bool lead = tid == 128 + 128 * half;
       int i = 0;
       bool ok = true;
@@ -643,85 +706,79 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         const int* s_tin = sh.tin[un & 1];
         const int base = a.mode == QB_CROSS ? u.len : u.len - u.n;
         // positions below `open` are seen by every row of the tile
-        const int open = a.mode == QB_CHAIN ? base + u.rt * (N / a.gqa) + 1 : base;
+        const int open = a.mode == QB_CHAIN ? base + u.rt * (N >> a.gqa_shift) + 1 : base;
         if (!meet(half)) break;  // the last unit's references are no longer read
-        if (tok < NH) sh.neg_m[col0 + tok] = -QB_NONE;
+        if (tok < NH) sh.neg_m[col0 + tok] = 0.f;
+        uint32_t unset = tok < CH ? (1u << NC) - 1u : 0u;  // by chunk: row `tok` of it has seen nothing yet, M = 0
         if (!meet(half)) break;
         uint64_t l2[NH / 2], z2[NH / 2];
 #pragma unroll
         for (int j = 0; j < NH / 2; ++j) l2[j] = z2[j] = 0ull;
         for (int t = u.t0; t < u.t1; ++t, ++i) {
-          const int st = i % QB_STAGES, buf = i & 1, use = i >> 1;
-          const uint8_t* meta = s_stage + st * QB_STAGE_BYTES + meta_off;
-          if (!(ok = wait(&sh.full[st], i / QB_STAGES))) break;
-          const float2 km = __half22float2(*reinterpret_cast<const __half2*>(meta));
-          const float2 vm = __half22float2(*reinterpret_cast<const __half2*>(meta + 4 * P));
-          arrive(&sh.empty[st]);
-          const int pos = t * QB_TOK + tok;
+          const int buf = i & 1, use = i >> 1;
           const bool masked = (t + 1) * QB_TOK > open;
           int key_tin = 0;
           unsigned key_size = 0x7fffffffu;
-          if (masked) {
-            if (pos >= u.len) {
+          if (__builtin_expect(masked, 0)) {
+            const int d = t * QB_TOK + tok - base;
+            if (d + base >= u.len) {
               key_size = 0u;
-            } else if (pos >= base) {
-              const int d = pos - base;
+            } else if (d >= 0) {
               const int2 ts = a.mode == QB_TREE ? a.ws.tree[u.c0 + d] : make_int2(d, u.n - d);
               key_tin = ts.x;
               key_size = (unsigned)ts.y;
             }
           }
-          const float sv = vm.x == 0.f ? 5.9604644775390625e-08f : vm.x;
-          const float ls = __log2f(sv), inv = __frcp_rn(sv);
-          const float sk = km.x * unscale, kmid = fmaf(1.5f, km.x, km.y), zc = inv * fmaf(1.5f, sv, vm.y);
-          const uint64_t sk2 = f2pk(sk, sk), kmid2 = f2pk(kmid, kmid), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
-                         zc2 = f2pk(zc, zc);
           if (!(ok = wait(&sh.s_done[buf], use))) break;
           tc_fence_after();
+          const float(*tc)[QB_TOK] = sh.tok[i & 3];
+          const float sk = tc[QB_C_SK][tok] * unscale, kmid = tc[QB_C_KMID][tok], ls = tc[QB_C_LS][tok],
+                      inv = tc[QB_C_INV][tok], zc = tc[QB_C_ZC][tok];
+          const uint64_t sk2 = f2pk(sk, sk), kmid2 = f2pk(kmid, kmid), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
+                         zc2 = f2pk(zc, zc);
           uint8_t* p_hi = s_p + (2 * buf) * QB_PBUF + tok * 128;
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const int col = col0 + c * CH;
             float x[CH];
-            qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col, x);
-            uint32_t see = 0xffffffffu;
-            if (masked) {
-              see = 0u;
-#pragma unroll
-              for (int j = 0; j < CH; ++j) see |= ((unsigned)(s_tin[col + j] - key_tin) < key_size ? 1u : 0u) << j;
-            }
-            float top = -INFINITY;
-            auto logits = [&](bool raw) {  // x: a + log2 s - M (raw: without M)
+            auto logits = [&]() {  // x: a + log2 s - M, -infinity where the row does not see the token
+              qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col, x);
 #pragma unroll
               for (int j = 0; j < CH; j += 4) {
                 const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col + j);
-                float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + col + j);
-                if (raw) nm = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + col + j);
                 const uint64_t u0 = f2fma(kmid2, f2pk(sq.x, sq.y), f2add(f2pk(nm.x, nm.y), ls2));
                 const uint64_t u1 = f2fma(kmid2, f2pk(sq.z, sq.w), f2add(f2pk(nm.z, nm.w), ls2));
                 const float2 d0 = f2up(f2fma(sk2, f2pk(x[j], x[j + 1]), u0));
                 const float2 d1 = f2up(f2fma(sk2, f2pk(x[j + 2], x[j + 3]), u1));
                 x[j] = d0.x; x[j + 1] = d0.y; x[j + 2] = d1.x; x[j + 3] = d1.y;
               }
-              if (masked) {
+              if (__builtin_expect(masked, 0)) {
 #pragma unroll
-                for (int j = 0; j < CH; ++j) x[j] = (see >> j) & 1u ? x[j] : -INFINITY;
+                for (int j = 0; j < CH; ++j) x[j] = (unsigned)(s_tin[col + j] - key_tin) < key_size ? x[j] : -INFINITY;
               }
             };
-            logits(false);
+            auto weights = [&]() {
+#pragma unroll
+              for (int j = 0; j < CH; ++j) x[j] = qb_ex2(x[j]);
+            };
+            logits();
+            float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < CH; ++j) top = fmaxf(top, x[j]);
-            const bool mine = __any_sync(FULLM, top > QB_TRIGGER);
+            // whether any weight of the chunk's 128 tokens passes the limit: voted on while the weights are taken
+            const bool mine = __any_sync(FULLM, top > QB_TRIGGER || ((unset >> c) & 1u));
             int* votes = sh.vote[half][round & 1];
             if (lane == 0) votes[q4] = mine;
-            if (!(ok = meet(half))) break;
+            arrive(&sh.group[half]);
+            weights();
+            if (!(ok = wait(&sh.group[half], round++))) break;
             const int4 v4 = *reinterpret_cast<const int4*>(votes);
             const bool move = (v4.x | v4.y | v4.z | v4.w) != 0;
             if (lead) sh.moved[i & 3][half * NC + c] = move;
-            if (move) {
-              // the chunk's references are set anew: column maxima over the 128 tokens
-              qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col, x);
-              logits(true);
+            if (__builtin_expect(move, 0)) {
+              // the chunk's references move up to the column maxima over the 128 tokens
+              logits();
               int col_max = 0;
 #pragma unroll
               for (int j = 0; j < CH; ++j) {
@@ -731,22 +788,27 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
               if (lane < CH) sh.red[half][q4][lane] = col_max;
               if (!(ok = meet(half))) break;
               if (tok < CH) {
-                const int m = max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
-                                  max(sh.red[half][2][tok], sh.red[half][3][tok]));
-                const float old = -sh.neg_m[col + tok], now = fmaxf(old, qb_unordered(m) - QB_LIFT);
-                sh.neg_m[col + tok] = -now;
-                sh.scale[i & 3][col + tok] = qb_ex2(old - now);
+                const float m = qb_unordered(max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
+                                                 max(sh.red[half][2][tok], sh.red[half][3][tok])));
+                const bool fresh = (unset >> c) & 1u;
+                const float by = (fresh ? m > -INFINITY : m > QB_LIFT) ? m - QB_LIFT : 0.f;
+                if (fresh && m > -INFINITY) unset &= ~(1u << c);
+                sh.neg_m[col + tok] -= by;
+                sh.delta[half][tok] = by;
+                sh.scale[i & 3][col + tok] = fresh ? 1.f : qb_ex2(-by);  // nothing to scale yet
               }
               if (!(ok = meet(half))) break;
-              qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col, x);
-              logits(false);
 #pragma unroll
               for (int j = 0; j < CH; j += 2) {
                 const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col + j);
+                const float2 by = *reinterpret_cast<const float2*>(sh.delta[half] + j);
                 const uint64_t f2 = f2pk(f.x, f.y);
                 l2[(c * CH + j) / 2] = f2mul(l2[(c * CH + j) / 2], f2);
                 z2[(c * CH + j) / 2] = f2mul(z2[(c * CH + j) / 2], f2);
+                x[j] -= by.x;
+                x[j + 1] -= by.y;
               }
+              weights();
             }
             if (c == NC - 1) {  // the scores are in registers
               tc_fence_before();
@@ -754,35 +816,25 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             }
             if (c == 0 && use && !(ok = wait(&sh.o_done[buf], use - 1))) break;
 #pragma unroll
-            for (int j = 0; j < CH; ++j) x[j] = qb_ex2(x[j]);
-            if (!masked) {
-#pragma unroll
-              for (int j = 0; j < CH; j += 2) {
-                const uint64_t w2 = f2pk(x[j], x[j + 1]);
-                l2[(c * CH + j) / 2] = f2fma(w2, inv2, l2[(c * CH + j) / 2]);
-                z2[(c * CH + j) / 2] = f2fma(w2, zc2, z2[(c * CH + j) / 2]);
-              }
-            } else {  // an unseen token adds exactly nothing, whatever its scale and zero are
-#pragma unroll
-              for (int j = 0; j < CH; j += 2) {
-                const bool v0 = (see >> j) & 1u, v1 = (see >> (j + 1)) & 1u;
-                l2[(c * CH + j) / 2] = f2add(l2[(c * CH + j) / 2], f2pk(v0 ? x[j] * inv : 0.f, v1 ? x[j + 1] * inv : 0.f));
-                z2[(c * CH + j) / 2] = f2add(z2[(c * CH + j) / 2], f2pk(v0 ? x[j] * zc : 0.f, v1 ? x[j + 1] * zc : 0.f));
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < CH; j += 8) {
+            for (int j = 0; j < CH; j += 8) {  // two fp16 halves of every weight
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const float w0 = x[j + 2 * k], w1 = x[j + 2 * k + 1];
                 hi[k] = qb_half2(w0, w1);
                 const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-                lo[k] = qb_half2(w0 - back.x, w1 - back.y);
+                const float2 r = f2up(f2sub(f2pk(w0, w1), f2pk(back.x, back.y)));
+                lo[k] = qb_half2(r.x, r.y);
               }
               const int at = (((col + j) >> 3) ^ (tok & 7)) << 4;
               *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
               *reinterpret_cast<uint4*>(p_hi + QB_PBUF + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < CH; j += 2) {
+              const uint64_t w2 = f2pk(x[j], x[j + 1]);
+              l2[(c * CH + j) / 2] = f2fma(w2, inv2, l2[(c * CH + j) / 2]);
+              z2[(c * CH + j) / 2] = f2fma(w2, zc2, z2[(c * CH + j) / 2]);
             }
           }
           if (!ok) break;
@@ -832,91 +884,92 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       // ---- accumulation: one channel a thread ----
       const int q4 = warp & 3, wt = tid - 384;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
-      const int ch = 8 * (lane & 15) + 2 * q4 + (lane >> 4);
       constexpr int TPR = 128 / N;  // threads a query row
-      const int row = wt / TPR, part = wt % TPR;
-      // queries of unit `un` into its buffer, with their sums and the tile's exponent
-      auto load_queries = [&](int un, const QbUnit& u) {
-        const int R = u.rt * N + row, tk = R / a.gqa;
-        const bool valid = tk < u.n;
-        const float* src = a.ws.q + ((size_t)(u.c0 + (valid ? tk : 0)) * a.n_q_heads + u.h * a.gqa + R % a.gqa) * D + part * N;
-        float m = 0.f, s = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < N; j += 4) {
-          const float4 v = valid ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-          s += (v.x + v.y) + (v.z + v.w);
-          const float w[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) m = w[k] <= 3.0e38f ? fmaxf(m, w[k]) : m;  // of the finite ones
-        }
-#pragma unroll
-        for (int d = 1; d < TPR; d <<= 1) s += __shfl_xor_sync(FULLM, s, d);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(FULLM, m, d));
-        if (lane == 0) sh.qmax[q4] = m;
-        if (!meet(2)) return false;
-        m = fmaxf(fmaxf(sh.qmax[0], sh.qmax[1]), fmaxf(sh.qmax[2], sh.qmax[3]));
-        // the largest at 2^13 .. 2^14
-        const int e = m > 0.f ? min(100, max(-100, 13 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
-        const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
-        uint8_t* dst = s_q + (un & 1) * N * 512 + row * 128;
-#pragma unroll
-        for (int j = 0; j < N; j += 16) {
-          float v[16];
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            const float4 x = valid ? *reinterpret_cast<const float4*>(src + j + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[k] = x.x * scale; v[k + 1] = x.y * scale; v[k + 2] = x.z * scale; v[k + 3] = x.w * scale;
-          }
-          // K order of the expanded keys: channels f and 8 + f of a 16-channel word side by side
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int f = 0; f < 8; ++f) {
-            hi[f] = qb_half2(v[f], v[8 + f]);
-            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[f]));
-            lo[f] = qb_half2(v[f] - back.x, v[8 + f] - back.y);
-          }
-          const int w = (part * N + j) >> 4;  // 16-channel word
-          uint8_t* d = dst + (w >> 2) * N * 128;
-          const int c0 = ((2 * (w & 3)) ^ (row & 7)) << 4, c1 = ((2 * (w & 3) + 1) ^ (row & 7)) << 4;
-          *reinterpret_cast<uint4*>(d + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(d + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-          *reinterpret_cast<uint4*>(d + N * 256 + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          *reinterpret_cast<uint4*>(d + N * 256 + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-        }
-        if (part == 0) {
-          sh.sumq[un & 1][row] = s;
-          sh.tin[un & 1][row] = !valid ? 0 : a.mode == QB_TREE ? a.ws.tree[u.c0 + tk].x : a.mode == QB_CHAIN ? tk : 0;
-        }
-        if (wt == 0) sh.unscale[un & 1] = __uint_as_float((uint32_t)(127 - e) << 23);
-        fence_proxy_async();
-        arrive(&sh.q_ready[un & 1]);
-        return meet(2);  // qmax may be written again
-      };
-      bool ok = wait(&sh.unit_full[0], 0);
-      QbUnit u = sh.unit[0];
-      if (ok) ok = load_queries(0, u);
+      const int row = wt / TPR, part = wt % TPR, gs = a.gqa_shift, gm = (1 << gs) - 1;
+      // channel `wt` is held by the thread of tensor-memory lane 16 f + g (f = channel % 8, g = channel / 8)
+      const int from = 16 * (wt & 7) + (wt >> 3);
+      QbUnit u{};
       int i = 0;
-      for (int un = 0; ok; ++un) {
-        if (!(ok = wait(&sh.unit_full[(un + 1) % QB_UNITS], (un + 1) / QB_UNITS))) break;
+      // round un: the queries of unit un + 1 into their buffer, then unit un
+      for (int un = -1;; ++un) {
+        if (!wait(&sh.unit_full[(un + 1) % QB_UNITS], (un + 1) / QB_UNITS)) break;
         const QbUnit next = sh.unit[(un + 1) % QB_UNITS];
-        arrive(&sh.unit_free[un % QB_UNITS]);
-        if (next.t1 > next.t0 && !(ok = load_queries(un + 1, next))) break;
-        float acc[N];
+        arrive(&sh.unit_free[(un + 1) % QB_UNITS]);
+        if (next.t1 > next.t0) {
+          const int R = next.rt * N + row, tk = R >> gs, buf = (un + 1) & 1;
+          const bool valid = tk < next.n;
+          const float* src =
+              a.ws.q + ((size_t)(next.c0 + (valid ? tk : 0)) * a.n_q_heads + next.h * a.gqa + (R & gm)) * D + part * N;
+          float m = 0.f, s = 0.f;
+#pragma unroll 4
+          for (int j = 0; j < N; j += 4) {
+            const float4 v = valid ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            s += (v.x + v.y) + (v.z + v.w);
+            const float w[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
 #pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] = 0.f;
-        for (int t = u.t0; t < u.t1; ++t, ++i) {
-          const int buf = i & 1, use = i >> 1;
-          if (!(ok = wait(&sh.o_done[buf], use))) break;
-          tc_fence_after();
+            for (int k = 0; k < 4; ++k) m = w[k] <= 3.0e38f ? fmaxf(m, w[k]) : m;  // of the finite ones
+          }
 #pragma unroll
-          for (int c = 0; c < N / CH; ++c) {
-            float o[CH];
-            qb_tmem_ld<CH>(tmem + lanes + T_O + 64 * buf + c * CH, o);
-            if (sh.moved[i & 3][c]) {
+          for (int d = 1; d < TPR; d <<= 1) s += __shfl_xor_sync(FULLM, s, d);
 #pragma unroll
-              for (int j = 0; j < CH; ++j) acc[c * CH + j] = fmaf(acc[c * CH + j], sh.scale[i & 3][c * CH + j], o[j]);
-            } else {
+          for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(FULLM, m, d));
+          if (lane == 0) sh.qmax[buf][q4] = m;
+          if (!meet(2)) break;
+          m = fmaxf(fmaxf(sh.qmax[buf][0], sh.qmax[buf][1]), fmaxf(sh.qmax[buf][2], sh.qmax[buf][3]));
+          // the largest at 2^13 .. 2^14
+          const int e = m > 0.f ? min(100, max(-100, 13 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
+          const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
+          uint8_t* dst = s_q + buf * N * 512 + row * 128;
+#pragma unroll 1
+          for (int j = 0; j < N; j += 16) {
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+              const float4 x = valid ? *reinterpret_cast<const float4*>(src + j + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+              v[k] = x.x * scale; v[k + 1] = x.y * scale; v[k + 2] = x.z * scale; v[k + 3] = x.w * scale;
+            }
+            // K order of the expanded keys: channels f and 8 + f of a 16-channel word side by side
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int f = 0; f < 8; ++f) {
+              hi[f] = qb_half2(v[f], v[8 + f]);
+              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[f]));
+              lo[f] = qb_half2(v[f] - back.x, v[8 + f] - back.y);
+            }
+            const int w = (part * N + j) >> 4;  // 16-channel word
+            uint8_t* d = dst + (w >> 2) * N * 128;
+            const int c0 = ((2 * (w & 3)) ^ (row & 7)) << 4, c1 = ((2 * (w & 3) + 1) ^ (row & 7)) << 4;
+            *reinterpret_cast<uint4*>(d + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(d + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+            *reinterpret_cast<uint4*>(d + N * 256 + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(d + N * 256 + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+          }
+          if (part == 0) {
+            sh.sumq[buf][row] = s;
+            sh.tin[buf][row] =
+                !valid ? 0 : a.mode == QB_TREE ? a.ws.tree[next.c0 + tk].x : a.mode == QB_CHAIN ? tk : 0;
+          }
+          if (wt == 0) sh.unscale[buf] = __uint_as_float((uint32_t)(127 - e) << 23);
+          fence_proxy_async();
+          arrive(&sh.q_ready[buf]);
+        }
+        if (un >= 0) {
+          float acc[N];
+#pragma unroll
+          for (int j = 0; j < N; ++j) acc[j] = 0.f;
+          bool ok = true;
+          for (int t = u.t0; t < u.t1; ++t, ++i) {
+            const int buf = i & 1, use = i >> 1;
+            if (!(ok = wait(&sh.o_done[buf], use))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < N / CH; ++c) {
+              float o[CH];
+              qb_tmem_ld<CH>(tmem + lanes + T_O + 64 * buf + c * CH, o);
+              if (sh.moved[i & 3][c]) {
+#pragma unroll
+                for (int j = 0; j < CH; ++j) acc[c * CH + j] *= sh.scale[i & 3][c * CH + j];
+              }
 #pragma unroll
               for (int j = 0; j < CH; j += 2) {
                 const float2 s = f2up(f2add(f2pk(acc[c * CH + j], acc[c * CH + j + 1]), f2pk(o[j], o[j + 1])));
@@ -924,38 +977,43 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
                 acc[c * CH + j + 1] = s.y;
               }
             }
+            tc_fence_before();
+            arrive(&sh.o_free[buf]);
           }
-          tc_fence_before();
-          arrive(&sh.o_free[buf]);
-        }
-        if (!ok || !(ok = wait(&sh.lz_ready, un))) break;
-        const bool whole = u.t0 == 0 && u.t1 == u.nt;
-        float* part_base = a.ws.part + (size_t)(2 * blockIdx.x + (u.t0 == 0 ? 1 : 0)) * N * (D + 2);
+          if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float l = (sh.lsum[0][j] + sh.lsum[1][j]) + (sh.lsum[2][j] + sh.lsum[3][j]);
-          const float z = (sh.zsum[0][j] + sh.zsum[1][j]) + (sh.zsum[2][j] + sh.zsum[3][j]);
-          const float o = acc[j] + z;
-          if (whole) {
-            const int R = u.rt * N + j, tk = R / a.gqa;
-            if (tk < u.n)
-              a.out[((size_t)(u.c0 + tk) * a.n_q_heads + u.h * a.gqa + R % a.gqa) * D + ch] = l != 0.f ? o / l : 0.f;
-          } else {
-            part_base[j * D + ch] = o;
-            if (wt == j) {
-              part_base[N * D + j] = l;
-              part_base[N * D + N + j] = sh.m_out[j];
+          for (int j = 0; j < N; ++j) s_out[j * D + wt] = acc[j];
+          if (!wait(&sh.lz_ready, un)) break;
+          const bool whole = u.t0 == 0 && u.t1 == u.nt;
+          float* part_out = a.ws.part + (size_t)(2 * blockIdx.x + (u.t0 == 0 ? 1 : 0)) * N * (D + 2);
+          if (wt < N) {
+            const float l = (sh.lsum[0][wt] + sh.lsum[1][wt]) + (sh.lsum[2][wt] + sh.lsum[3][wt]);
+            const float z = (sh.zsum[0][wt] + sh.zsum[1][wt]) + (sh.zsum[2][wt] + sh.zsum[3][wt]);
+            sh.row_z[wt] = z;
+            sh.row_f[wt] = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+            if (!whole) {
+              part_out[N * D + wt] = l;
+              part_out[N * D + N + wt] = sh.m_out[wt];
             }
           }
+          arrive(&sh.lz_free);
+          if (!meet(2)) break;
+          const int rows = min(N, (u.n << gs) - u.rt * N);
+          float* out = a.out + ((size_t)u.c0 * a.n_q_heads + u.h * a.gqa) * D + wt;
+#pragma unroll 4
+          for (int j = 0; j < rows; ++j) {
+            const float o = (s_out[j * D + from] + sh.row_z[j]) * sh.row_f[j];
+            const int R = u.rt * N + j;
+            if (whole) out[((size_t)(R >> gs) * a.n_q_heads + (R & gm)) * D] = o;
+            else part_out[j * D + wt] = o;
+          }
+          if (!meet(2)) break;  // the staging rows may be written again
         }
-        arrive(&sh.lz_free);
-        if (next.t1 == next.t0) {
-          arrive(&sh.unit_free[(un + 1) % QB_UNITS]);
-          break;
-        }
+        if (next.t1 == next.t0) break;
         u = next;
       }
     } else if (warp == 16) {
+      if constexpr (N == 64) qb_registers<56, false>();
       // ---- page copies, and the list of units one ahead of them ----
       QbUnit u = qb_locate<N>(a, first, lane), ahead;
       long long left = n_tiles;
@@ -1002,7 +1060,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       }
       if (!ok)  // no copy in flight when the CTA ends
         for (int k = max(0, i - QB_STAGES); k < i; ++k) mbar_wait_bounded(&sh.full[k % QB_STAGES], (k / QB_STAGES) & 1);
+    } else if (warp > 17) {
+      if constexpr (N == 64) qb_registers<56, false>();
     } else {
+      if constexpr (N == 64) qb_registers<56, false>();
       // ---- MMA issue ----
       constexpr uint32_t I_QK = qb_idesc(N, false), I_PV = qb_idesc(N, true);
       auto pv = [&](int i) {
@@ -1010,13 +1071,14 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         if (!wait(&sh.v_ready[buf], use) || !wait(&sh.p_ready[buf], use) || (use && !wait(&sh.o_free[buf], use - 1)))
           return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (qb_elect()) {
           const uint64_t hi = sw128_desc(s_p + (2 * buf) * QB_PBUF), lo = sw128_desc(s_p + (2 * buf + 1) * QB_PBUF);
           const uint32_t av = tmem + T_V + 64 * buf, d = tmem + T_O + 64 * buf;
+          // loops on purpose: the roles' code has to fit the instruction cache together
+#pragma unroll 1
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, av + 8 * k, lo + k * (2048 >> 4), I_PV, k > 0);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, av + 8 * k, hi + k * (2048 >> 4), I_PV, true);
+            for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, av + 8 * k, (p ? hi : lo) + k * (2048 >> 4), I_PV, p + k > 0);
           tc_commit(&sh.o_done[buf]);
         }
         __syncwarp();
@@ -1035,14 +1097,14 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           const int buf = i & 1, use = i >> 1;
           if (!(ok = wait(&sh.k_ready[buf], use) && (!use || wait(&sh.s_free[buf], use - 1)))) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (qb_elect()) {
             const uint32_t ak = tmem + T_K + 64 * buf, d = tmem + T_S + 64 * buf;
+            const uint64_t q = sw128_desc(qt);
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p)  // lo, then hi: 4 steps of 16 channels in each of two halves
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_f16_ts(d, ak + 8 * k, sw128_desc(qt + (2 + (k >> 2)) * N * 128) + (k & 3) * 2, I_QK, k > 0);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_f16_ts(d, ak + 8 * k, sw128_desc(qt + (k >> 2) * N * 128) + (k & 3) * 2, I_QK, true);
+              for (int k = 0; k < 8; ++k)
+                tc_mma_f16_ts(d, ak + 8 * k, q + ((p ? 0 : 2) + (k >> 2)) * (N * 128 >> 4) + (k & 3) * 2, I_QK, p + k > 0);
             tc_commit(&sh.s_done[buf]);
           }
           __syncwarp();
@@ -1051,7 +1113,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       }
       if (ok) ok = pv(i - 1);
       if (!ok) {  // let the tensor cores finish before their memory is freed
-        if (lane == 0) tc_commit(&sh.last);
+        if (qb_elect()) tc_commit(&sh.last);
         __syncwarp();
         mbar_wait_bounded(&sh.last, 0);
       }
@@ -1075,8 +1137,9 @@ __global__ void __launch_bounds__(D) qb_combine_kernel(QbArgs a, int grid) {
   __shared__ long long s_u0;
   pdl_wait();
   const long long total = a.ws.tiles[a.n_seqs];
+  const QbSlices slices(total, grid);
   const int k = blockIdx.x;
-  const long long start = total * k / grid, end = total * (k + 1) / grid;
+  const long long start = slices.start(k), end = slices.start(k + 1);
   if (end == start) return;
   if (threadIdx.x < 32) {
     const QbUnit u = qb_locate<N>(a, end - 1, threadIdx.x);
@@ -1089,25 +1152,31 @@ __global__ void __launch_bounds__(D) qb_combine_kernel(QbArgs a, int grid) {
   const QbUnit u = s_u;
   const long long u0 = s_u0, u1 = u0 + u.nt;
   if (u1 <= end || u0 < start) return;
-  int j1 = k + 1;  // the slice after the last one that holds a part (an empty slice holds none)
-  while (j1 < grid && total * j1 / grid < u1) ++j1;
+  int parts = 1;  // slices after k are not empty before u1: sizes differ by one, larger ones first
+  while (slices.start(k + parts) < u1) ++parts;
+  const float* first = a.ws.part + (size_t)(2 * k + 1) * N * (D + 2);
+  const float* rest = a.ws.part + (size_t)(2 * k) * N * (D + 2);  // + 2 j slots: slice k + j
+  const size_t step = (size_t)2 * N * (D + 2);
   for (int r = blockIdx.y * QB_JOIN_ROWS; r < (int)(blockIdx.y + 1) * QB_JOIN_ROWS; ++r) {
-    const int R = u.rt * N + r, tk = R / a.gqa;
+    const int R = u.rt * N + r, tk = R >> a.gqa_shift;
     if (tk >= u.n) return;
-    float m = QB_NONE;
-    for (int j = k; j < j1; ++j) {
-      if (total * j / grid == total * (j + 1) / grid) continue;
-      m = fmaxf(m, a.ws.part[(size_t)(2 * j + (j == k)) * N * (D + 2) + N * D + N + r]);
+    // a part without visible tokens (l = 0) has no reference
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int j = 0; j < parts; ++j) {
+      const float* p = (j ? rest + j * step : first) + N * D;
+      m = fmaxf(m, p[r] != 0.f ? p[N + r] : -INFINITY);
     }
     float o = 0.f, l = 0.f;
-    for (int j = k; j < j1; ++j) {
-      if (total * j / grid == total * (j + 1) / grid) continue;
-      const float* p = a.ws.part + (size_t)(2 * j + (j == k)) * N * (D + 2);
-      const float f = exp2f(p[N * D + N + r] - m);
+#pragma unroll 4
+    for (int j = 0; j < parts; ++j) {
+      const float* p = j ? rest + j * step : first;
+      const float pl = p[N * D + r], f = pl != 0.f ? exp2f(p[N * D + N + r] - m) : 0.f;
       o = fmaf(p[r * D + threadIdx.x], f, o);
-      l = fmaf(p[N * D + r], f, l);
+      l = fmaf(pl, f, l);
     }
-    a.out[((size_t)(u.c0 + tk) * a.n_q_heads + u.h * a.gqa + R % a.gqa) * D + threadIdx.x] = l != 0.f ? o / l : 0.f;
+    a.out[((size_t)(u.c0 + tk) * a.n_q_heads + u.h * a.gqa + (R & ((1 << a.gqa_shift) - 1))) * D + threadIdx.x] =
+        l != 0.f ? o / l : 0.f;
   }
 }
 
@@ -1145,7 +1214,8 @@ cudaError_t launch_query_block(const PageGeom& g, int n_q_heads, int n_seqs, int
                                int max_len, const int32_t* table, RotDev rot_k, const uint8_t* pool, void* ws_base,
                                float* o_rot, unsigned* err, cudaStream_t s) {
   const int gqa = n_q_heads / g.n_kv_heads, rows = qb_rows(max_q, gqa), grid = device_sm_count();
-  QbArgs a{g, n_q_heads, gqa, n_seqs, n_total, max_q, max_len, mode, cu_q, lens, table, pool, {}, o_rot, err};
+  QbArgs a{g, n_q_heads, gqa, n_seqs, n_total, max_q, max_len, mode, __builtin_ctz(gqa), __builtin_ctz(g.page_tokens),
+           cu_q, lens, table, pool, {}, o_rot, err};
   qb_layout(ws_base, n_seqs, n_total, n_q_heads, rows, grid, &a.ws);
   return rows == 16   ? qb_launch<16>(a, parents, q, dtype, rot_k, grid, s)
          : rows == 32 ? qb_launch<32>(a, parents, q, dtype, rot_k, grid, s)
