@@ -414,33 +414,39 @@ __device__ __forceinline__ void qb_tmem_ld(uint32_t taddr, float (&v)[C]) {
 }
 
 // ---------------------------------------------------------------------------
-// Expansion of 2-bit codes: field F (bits 2F, 2F + 1) of both 16-bit halves of x as
-// the fp16 pair c - 1.5.  The field lands in the mantissa of 2^k + c (exact), from
-// which 2^k + 1.5 is subtracted (exact); fields that straddle the exponent bits are
-// taken from the byte-swapped halves.
+// Expansion of 2-bit codes, both 16-bit halves of a register at once.
+// Keys: field f (bits 2f, 2f + 1 of a half) masked in place is the subnormal fp16
+// c * 2^(qb_bit(f) - 24) - one instruction a register; fields that straddle the
+// exponent bits are taken from the byte-swapped halves.  The powers of two are
+// compensated in the queries (exactly).  The queries' signs are mixed, so codes that
+// are not centred cost the sums nothing.
+// Values: the weights are positive, so the codes are centred: a field masked into the
+// mantissa of 2^k + c (exact), from which 2^k + 1.5 is subtracted (exact).
 // ---------------------------------------------------------------------------
-template <int F>
-__device__ __forceinline__ uint32_t qb_field(uint32_t x, uint32_t x_swapped) {
-  constexpr int bit = F == 0 ? 8 : F <= 4 ? 2 * F : 2 * F - 8;  // 2, 4, 6 or 8
-  constexpr bool swapped = F == 0 || F >= 5;
-  constexpr uint32_t mask = 0x00030003u << bit;
-  constexpr uint32_t e = (uint32_t)(25 - bit) << 10;            // 2^(10 - bit): one unit of c at that bit
-  constexpr uint32_t magic = e | (e << 16);
-  // 2^k + 1.5: mantissa 1.5 * 2^bit
-  constexpr uint32_t off16 = e + (3u << (bit - 1)), off = off16 | (off16 << 16);
-  const uint32_t v = ((swapped ? x_swapped : x) & mask) | magic;
-  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), __halves2half2(__ushort_as_half(off & 0xffff), __ushort_as_half(off & 0xffff)));
-  return *reinterpret_cast<const uint32_t*>(&d);
-}
+__host__ __device__ constexpr int qb_bit(int f) { return f == 0 ? 8 : f <= 4 ? 2 * f : 2 * f - 8; }  // 2, 4, 6 or 8
+__host__ __device__ constexpr bool qb_swapped(int f) { return f == 0 || f >= 5; }
 __device__ __forceinline__ uint32_t qb_swap(uint32_t x) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %1, 0x2301;" : "=r"(d) : "r"(x));
   return d;
 }
-
-__device__ __forceinline__ uint32_t qb_permute(uint32_t x, uint32_t order) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(d) : "r"(x), "r"(order));
+template <int F>
+__device__ __forceinline__ uint32_t qb_key_field(uint32_t x, uint32_t x_swapped) {
+  return (qb_swapped(F) ? x_swapped : x) & (0x00030003u << qb_bit(F));
+}
+// The field at bits BIT, BIT + 1 as c - 1.5.
+template <int BIT>
+__device__ __forceinline__ uint32_t qb_centred(uint32_t x) {
+  constexpr uint32_t e = (uint32_t)(25 - BIT) << 10;  // 2^(10 - BIT): one unit of c at that bit
+  constexpr uint32_t off = e + (3u << (BIT - 1));     // 2^(10 - BIT) + 1.5
+  const uint32_t v = (x & (0x00030003u << BIT)) | (e | (e << 16));
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v),
+                            __halves2half2(__ushort_as_half(off), __ushort_as_half(off)));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ float qb_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -459,35 +465,8 @@ __device__ __forceinline__ uint32_t qb_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// One try without a time hint: the roles hand tiles to one another every few hundred
-// nanoseconds, and a suspension with a long hint was measured to wake up microseconds late.
-__device__ __forceinline__ bool qb_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ unsigned long long qb_now() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-constexpr unsigned long long QB_WAIT_NS = 2000000000ull;
-__device__ __forceinline__ bool qb_wait_slow(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = qb_now();
-  do {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (qb_try_wait(bar, parity)) return true;
-  } while (qb_now() - t0 < QB_WAIT_NS);
-  return false;
-}
-
-// A token's constants: key scale, key mid, log2 of the value scale, its reciprocal, value mid over value scale.
-enum { QB_C_SK, QB_C_KMID, QB_C_LS, QB_C_INV, QB_C_ZC };
+// A token's constants: key scale and zero, log2 of the value scale, its reciprocal, value mid over value scale.
+enum { QB_C_SK, QB_C_KZ, QB_C_LS, QB_C_INV, QB_C_ZC };
 
 // Register shares of a group of four warps (the block's total stays what it was launched with).
 template <int R, bool UP>
@@ -502,16 +481,16 @@ struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) int tin[2][N];
   alignas(16) float neg_m[N];       // -M of the running unit
   alignas(16) float scale[4][N];    // factors of the accumulated numerator for tile i (i % 4), where flagged
-  alignas(16) int moved[4][4];      // per chunk of rows: whether tile i moved a reference
+  alignas(8) int moved[4][2];       // per half of the rows: whether tile i (i % 4) moved a reference
   alignas(16) int vote[2][2][4];    // per half of the softmax warps: the warps' votes, two rounds
-  alignas(16) int red[2][4][16];    // per half: a chunk's column maxima per warp
-  alignas(16) float delta[2][16];   // per half: how far a chunk's references moved
+  alignas(16) int red[2][4][32];    // per half: the rows' maxima per warp
+  alignas(16) float delta[2][32];   // per half: how far the references moved
   alignas(16) float tok[4][5][QB_TOK];  // constants of tile i (i % 4): see QB_C_*
   alignas(16) float lsum[4][N];
   alignas(16) float zsum[4][N];
   alignas(16) float m_out[N];
   alignas(16) QbUnit unit[QB_UNITS];
-  float unscale[2];                 // 2^-E of the unit's queries
+  float unscale[2];                 // what the products of key codes and queries are scaled back by
   float qmax[2][4];
   float row_z[N], row_f[N];         // of the unit being written out
   alignas(8) uint64_t full[QB_STAGES];
@@ -583,12 +562,17 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
   const long long first = slices.start(blockIdx.x);
   const int n_tiles = (int)(slices.start(blockIdx.x + 1) - first);
 
-  // warp-uniform wait, bounded in time; a role that gives up ends, and with it, in time, the others
+  // warp-uniform bounded wait, kept short (it stands in many places); a role that gives up ends, and with
+  // it, in time, the others
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (__builtin_expect(__all_sync(FULLM, qb_try_wait(bar, parity & 1)), 1)) return true;
-    const bool ok = __all_sync(FULLM, qb_wait_slow(bar, parity & 1));
-    if (!ok && lane == 0) flag_error(a.err, ERR_TIMEOUT);
-    return ok;
+    int left = WAIT_LIMIT;
+#pragma unroll 1
+    while (!__all_sync(FULLM, mbar_try_wait(bar, parity & 1)))
+      if (--left == 0) {
+        if (lane == 0) flag_error(a.err, ERR_TIMEOUT);
+        return false;
+      }
+    return true;
   };
   auto arrive = [&](uint64_t* bar) {
     __syncwarp();
@@ -613,15 +597,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       // rows of the transposing loads: lane l gives row l % 8 of matrix l / 8; 16 tokens are 1152 bytes of either page size
       const int vt = (lane & 7) + ((lane >> 4) << 3), vh = (lane >> 3) & 1;
       const int v_off = (vt >> ps) * a.g.record + (32 << ps) + 32 * (vt & pm) + 16 * vh;
-      // this warp's value fields f = 2 warp, 2 warp + 1: byte order and shift that bring them to bits 2, 3 (see qb_field)
-      uint32_t v_order[2];
-      int v_shift[2];
-#pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        const int f = 2 * warp + o;
-        v_order[o] = f == 0 || f >= 5 ? 0x2301u : 0x3210u;
-        v_shift[o] = f == 0 ? 6 : f >= 5 ? 2 * f - 10 : 2 * f - 2;
-      }
+      // this warp's value fields 2 warp and 2 warp + 1 are bits 4 warp .. 4 warp + 3: rotated to bits 4 .. 7
+      const int v_rotate = (4 * warp - 4) & 31;
       for (int i = 0; i < n_tiles; ++i) {
         const int st = i % QB_STAGES, buf = i & 1, use = i >> 1;
         const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
@@ -637,7 +614,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
           float(*c)[QB_TOK] = sh.tok[i & 3];
           c[QB_C_SK][tok] = km.x;
-          c[QB_C_KMID][tok] = fmaf(1.5f, km.x, km.y);
+          c[QB_C_KZ][tok] = km.y;
           c[QB_C_LS][tok] = ls;
           c[QB_C_INV][tok] = inv;
           c[QB_C_ZC][tok] = zc;
@@ -652,14 +629,14 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t x = j ? w.y : w.x, y = qb_swap(x);
-            r[8 * j + 0] = qb_field<0>(x, y);
-            r[8 * j + 1] = qb_field<1>(x, y);
-            r[8 * j + 2] = qb_field<2>(x, y);
-            r[8 * j + 3] = qb_field<3>(x, y);
-            r[8 * j + 4] = qb_field<4>(x, y);
-            r[8 * j + 5] = qb_field<5>(x, y);
-            r[8 * j + 6] = qb_field<6>(x, y);
-            r[8 * j + 7] = qb_field<7>(x, y);
+            r[8 * j + 0] = qb_key_field<0>(x, y);
+            r[8 * j + 1] = qb_key_field<1>(x, y);
+            r[8 * j + 2] = qb_key_field<2>(x, y);
+            r[8 * j + 3] = qb_key_field<3>(x, y);
+            r[8 * j + 4] = qb_key_field<4>(x, y);
+            r[8 * j + 5] = qb_key_field<5>(x, y);
+            r[8 * j + 6] = qb_key_field<6>(x, y);
+            r[8 * j + 7] = qb_key_field<7>(x, y);
           }
           tmem_st16(tmem + lanes + T_K + 64 * buf + 16 * k, r);
         }
@@ -675,11 +652,13 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           ldsm_x4_trans(smem_u32(stage + v_off + 2304 * k + 1152), *reinterpret_cast<uint32_t(*)[4]>(raw + 4));
           const uint32_t ta = tmem + lanes + T_V + 64 * buf + 16 * k;
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {
+          for (int j = 0; j < 8; ++j) raw[j] = __funnelshift_r(raw[j], raw[j], v_rotate);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = qb_field<1>(qb_permute(raw[j], v_order[o]) >> v_shift[o], 0u);
-            tmem_st16x128_x4(ta + ((uint32_t)(16 * o) << 16), r);
-          }
+          for (int j = 0; j < 8; ++j) r[j] = qb_centred<4>(raw[j]);
+          tmem_st16x128_x4(ta, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[j] = qb_centred<6>(raw[j]);
+          tmem_st16x128_x4(ta + (16u << 16), r);
         }
         arrive(&sh.empty[st]);
         tmem_wait_st();
@@ -688,7 +667,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       }
     } else if (warp < 12) {
       // ---- softmax: one token a thread, rows col0 .. col0 + NH - 1 ----
-      if constexpr (N == 64) qb_registers<128, true>();
+      if constexpr (N == 64) qb_registers<136, true>();
       const int half = (warp - 4) >> 2, q4 = warp & 3, col0 = half * NH;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       const int tok = 32 * q4 + lane;
@@ -709,7 +688,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         const int open = a.mode == QB_CHAIN ? base + u.rt * (N >> a.gqa_shift) + 1 : base;
         if (!meet(half)) break;  // the last unit's references are no longer read
         if (tok < NH) sh.neg_m[col0 + tok] = 0.f;
-        uint32_t unset = tok < CH ? (1u << NC) - 1u : 0u;  // by chunk: row `tok` of it has seen nothing yet, M = 0
+        bool unset = tok < NH;  // row col0 + tok has seen nothing yet, and M = 0
         if (!meet(half)) break;
         uint64_t l2[NH / 2], z2[NH / 2];
 #pragma unroll
@@ -732,114 +711,104 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           if (!(ok = wait(&sh.s_done[buf], use))) break;
           tc_fence_after();
           const float(*tc)[QB_TOK] = sh.tok[i & 3];
-          const float sk = tc[QB_C_SK][tok] * unscale, kmid = tc[QB_C_KMID][tok], ls = tc[QB_C_LS][tok],
+          const float sk = tc[QB_C_SK][tok] * unscale, kz = tc[QB_C_KZ][tok], ls = tc[QB_C_LS][tok],
                       inv = tc[QB_C_INV][tok], zc = tc[QB_C_ZC][tok];
-          const uint64_t sk2 = f2pk(sk, sk), kmid2 = f2pk(kmid, kmid), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
+          const uint64_t sk2 = f2pk(sk, sk), kz2 = f2pk(kz, kz), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
                          zc2 = f2pk(zc, zc);
           uint8_t* p_hi = s_p + (2 * buf) * QB_PBUF + tok * 128;
+          float x[NH];
+          auto logits = [&]() {  // x: a + log2 s - M, -infinity where the row does not see the token
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const int col = col0 + c * CH;
-            float x[CH];
-            auto logits = [&]() {  // x: a + log2 s - M, -infinity where the row does not see the token
-              qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col, x);
+            for (int c = 0; c < NC; ++c)
+              qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col0 + c * CH, *reinterpret_cast<float(*)[CH]>(x + c * CH));
 #pragma unroll
-              for (int j = 0; j < CH; j += 4) {
-                const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col + j);
-                const float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + col + j);
-                const uint64_t u0 = f2fma(kmid2, f2pk(sq.x, sq.y), f2add(f2pk(nm.x, nm.y), ls2));
-                const uint64_t u1 = f2fma(kmid2, f2pk(sq.z, sq.w), f2add(f2pk(nm.z, nm.w), ls2));
-                const float2 d0 = f2up(f2fma(sk2, f2pk(x[j], x[j + 1]), u0));
-                const float2 d1 = f2up(f2fma(sk2, f2pk(x[j + 2], x[j + 3]), u1));
-                x[j] = d0.x; x[j + 1] = d0.y; x[j + 2] = d1.x; x[j + 3] = d1.y;
-              }
-              if (__builtin_expect(masked, 0)) {
+            for (int j = 0; j < NH; j += 4) {
+              const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col0 + j);
+              const float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + col0 + j);
+              const uint64_t u0 = f2fma(kz2, f2pk(sq.x, sq.y), f2add(f2pk(nm.x, nm.y), ls2));
+              const uint64_t u1 = f2fma(kz2, f2pk(sq.z, sq.w), f2add(f2pk(nm.z, nm.w), ls2));
+              const float2 d0 = f2up(f2fma(sk2, f2pk(x[j], x[j + 1]), u0));
+              const float2 d1 = f2up(f2fma(sk2, f2pk(x[j + 2], x[j + 3]), u1));
+              x[j] = d0.x; x[j + 1] = d0.y; x[j + 2] = d1.x; x[j + 3] = d1.y;
+            }
+            if (__builtin_expect(masked, 0)) {
 #pragma unroll
-                for (int j = 0; j < CH; ++j) x[j] = (unsigned)(s_tin[col + j] - key_tin) < key_size ? x[j] : -INFINITY;
-              }
-            };
-            auto weights = [&]() {
+              for (int j = 0; j < NH; ++j) x[j] = (unsigned)(s_tin[col0 + j] - key_tin) < key_size ? x[j] : -INFINITY;
+            }
+          };
+          logits();
+          float top = -INFINITY;
 #pragma unroll
-              for (int j = 0; j < CH; ++j) x[j] = qb_ex2(x[j]);
-            };
+          for (int j = 0; j < NH; j += 2) top = qb_max3(top, x[j], x[j + 1]);
+          // whether any weight of the 128 tokens passes the limit: voted on while the weights are taken
+          const bool mine = __any_sync(FULLM, top > QB_TRIGGER || unset);
+          int* votes = sh.vote[half][round & 1];
+          if (lane == 0) votes[q4] = mine;
+          arrive(&sh.group[half]);
+#pragma unroll
+          for (int j = 0; j < NH; ++j) x[j] = qb_ex2(x[j]);
+          if (!(ok = wait(&sh.group[half], round++))) break;
+          const int4 v4 = *reinterpret_cast<const int4*>(votes);
+          const bool move = (v4.x | v4.y | v4.z | v4.w) != 0;
+          if (lead) sh.moved[i & 3][half] = move;
+          if (__builtin_expect(move, 0)) {
+            // the references move up to the rows' maxima over the 128 tokens
             logits();
-            float top = -INFINITY;
+            int row_max = 0;
 #pragma unroll
-            for (int j = 0; j < CH; ++j) top = fmaxf(top, x[j]);
-            // whether any weight of the chunk's 128 tokens passes the limit: voted on while the weights are taken
-            const bool mine = __any_sync(FULLM, top > QB_TRIGGER || ((unset >> c) & 1u));
-            int* votes = sh.vote[half][round & 1];
-            if (lane == 0) votes[q4] = mine;
-            arrive(&sh.group[half]);
-            weights();
-            if (!(ok = wait(&sh.group[half], round++))) break;
-            const int4 v4 = *reinterpret_cast<const int4*>(votes);
-            const bool move = (v4.x | v4.y | v4.z | v4.w) != 0;
-            if (lead) sh.moved[i & 3][half * NC + c] = move;
-            if (__builtin_expect(move, 0)) {
-              // the chunk's references move up to the column maxima over the 128 tokens
-              logits();
-              int col_max = 0;
-#pragma unroll
-              for (int j = 0; j < CH; ++j) {
-                const int m = __reduce_max_sync(FULLM, qb_ordered(x[j]));
-                if (lane == j) col_max = m;
-              }
-              if (lane < CH) sh.red[half][q4][lane] = col_max;
-              if (!(ok = meet(half))) break;
-              if (tok < CH) {
-                const float m = qb_unordered(max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
-                                                 max(sh.red[half][2][tok], sh.red[half][3][tok])));
-                const bool fresh = (unset >> c) & 1u;
-                const float by = (fresh ? m > -INFINITY : m > QB_LIFT) ? m - QB_LIFT : 0.f;
-                if (fresh && m > -INFINITY) unset &= ~(1u << c);
-                sh.neg_m[col + tok] -= by;
-                sh.delta[half][tok] = by;
-                sh.scale[i & 3][col + tok] = fresh ? 1.f : qb_ex2(-by);  // nothing to scale yet
-              }
-              if (!(ok = meet(half))) break;
-#pragma unroll
-              for (int j = 0; j < CH; j += 2) {
-                const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col + j);
-                const float2 by = *reinterpret_cast<const float2*>(sh.delta[half] + j);
-                const uint64_t f2 = f2pk(f.x, f.y);
-                l2[(c * CH + j) / 2] = f2mul(l2[(c * CH + j) / 2], f2);
-                z2[(c * CH + j) / 2] = f2mul(z2[(c * CH + j) / 2], f2);
-                x[j] -= by.x;
-                x[j + 1] -= by.y;
-              }
-              weights();
+            for (int j = 0; j < NH; ++j) {
+              const int m = __reduce_max_sync(FULLM, qb_ordered(x[j]));
+              if (lane == j) row_max = m;
             }
-            if (c == NC - 1) {  // the scores are in registers
-              tc_fence_before();
-              arrive(&sh.s_free[buf]);
+            if (lane < NH) sh.red[half][q4][lane] = row_max;
+            if (!(ok = meet(half))) break;
+            if (tok < NH) {
+              const float m = qb_unordered(max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
+                                               max(sh.red[half][2][tok], sh.red[half][3][tok])));
+              const float by = (unset ? m > -INFINITY : m > QB_LIFT) ? m - QB_LIFT : 0.f;
+              sh.neg_m[col0 + tok] -= by;
+              sh.delta[half][tok] = by;
+              sh.scale[i & 3][col0 + tok] = unset ? 1.f : qb_ex2(-by);  // nothing to scale yet
+              if (m > -INFINITY) unset = false;
             }
-            if (c == 0 && use && !(ok = wait(&sh.o_done[buf], use - 1))) break;
+            if (!(ok = meet(half))) break;
 #pragma unroll
-            for (int j = 0; j < CH; j += 8) {  // two fp16 halves of every weight
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float w0 = x[j + 2 * k], w1 = x[j + 2 * k + 1];
-                hi[k] = qb_half2(w0, w1);
-                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-                const float2 r = f2up(f2sub(f2pk(w0, w1), f2pk(back.x, back.y)));
-                lo[k] = qb_half2(r.x, r.y);
-              }
-              const int at = (((col + j) >> 3) ^ (tok & 7)) << 4;
-              *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(p_hi + QB_PBUF + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-#pragma unroll
-            for (int j = 0; j < CH; j += 2) {
-              const uint64_t w2 = f2pk(x[j], x[j + 1]);
-              l2[(c * CH + j) / 2] = f2fma(w2, inv2, l2[(c * CH + j) / 2]);
-              z2[(c * CH + j) / 2] = f2fma(w2, zc2, z2[(c * CH + j) / 2]);
+            for (int j = 0; j < NH; j += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col0 + j);
+              const float2 by = *reinterpret_cast<const float2*>(sh.delta[half] + j);
+              const uint64_t f2 = f2pk(f.x, f.y);
+              l2[j / 2] = f2mul(l2[j / 2], f2);
+              z2[j / 2] = f2mul(z2[j / 2], f2);
+              x[j] = qb_ex2(x[j] - by.x);
+              x[j + 1] = qb_ex2(x[j + 1] - by.y);
             }
           }
-          if (!ok) break;
+          tc_fence_before();  // the scores are in registers
+          arrive(&sh.s_free[buf]);
+          if (use && !(ok = wait(&sh.o_done[buf], use - 1))) break;
+#pragma unroll
+          for (int j = 0; j < NH; j += 8) {  // two fp16 halves of every weight
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float w0 = x[j + 2 * k], w1 = x[j + 2 * k + 1];
+              hi[k] = qb_half2(w0, w1);
+              const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+              const float2 r = f2up(f2sub(f2pk(w0, w1), f2pk(back.x, back.y)));
+              lo[k] = qb_half2(r.x, r.y);
+            }
+            const int at = (((col0 + j) >> 3) ^ (tok & 7)) << 4;
+            *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(p_hi + QB_PBUF + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
           fence_proxy_async();
           arrive(&sh.p_ready[buf]);
+#pragma unroll
+          for (int j = 0; j < NH; j += 2) {
+            const uint64_t w2 = f2pk(x[j], x[j + 1]);
+            l2[j / 2] = f2fma(w2, inv2, l2[j / 2]);
+            z2[j / 2] = f2fma(w2, zc2, z2[j / 2]);
+          }
         }
         if (!ok) break;
         // the unit's l and sum p mid: over the warp's 32 tokens by exchange and halving, over the warps by the writer
@@ -916,8 +885,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           if (lane == 0) sh.qmax[buf][q4] = m;
           if (!meet(2)) break;
           m = fmaxf(fmaxf(sh.qmax[buf][0], sh.qmax[buf][1]), fmaxf(sh.qmax[buf][2], sh.qmax[buf][3]));
-          // the largest at 2^13 .. 2^14
-          const int e = m > 0.f ? min(100, max(-100, 13 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
+          // the largest at 2^8 .. 2^9, times up to 2^6 for the keys' fields
+          const int e = m > 0.f ? min(100, max(-100, 8 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
           const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
           uint8_t* dst = s_q + buf * N * 512 + row * 128;
 #pragma unroll 1
@@ -932,6 +901,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int f = 0; f < 8; ++f) {
+              v[f] *= (float)(1 << (8 - qb_bit(f)));
+              v[8 + f] *= (float)(1 << (8 - qb_bit(f)));
               hi[f] = qb_half2(v[f], v[8 + f]);
               const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[f]));
               lo[f] = qb_half2(v[f] - back.x, v[8 + f] - back.y);
@@ -949,7 +920,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             sh.tin[buf][row] =
                 !valid ? 0 : a.mode == QB_TREE ? a.ws.tree[next.c0 + tk].x : a.mode == QB_CHAIN ? tk : 0;
           }
-          if (wt == 0) sh.unscale[buf] = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (wt == 0) sh.unscale[buf] = __uint_as_float((uint32_t)(127 + 16 - e) << 23);
           fence_proxy_async();
           arrive(&sh.q_ready[buf]);
         }
@@ -966,7 +937,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             for (int c = 0; c < N / CH; ++c) {
               float o[CH];
               qb_tmem_ld<CH>(tmem + lanes + T_O + 64 * buf + c * CH, o);
-              if (sh.moved[i & 3][c]) {
+              if (sh.moved[i & 3][c / NC]) {
 #pragma unroll
                 for (int j = 0; j < CH; ++j) acc[c * CH + j] *= sh.scale[i & 3][c * CH + j];
               }
@@ -1013,7 +984,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         u = next;
       }
     } else if (warp == 16) {
-      if constexpr (N == 64) qb_registers<56, false>();
+      if constexpr (N == 64) qb_registers<40, false>();
       // ---- page copies, and the list of units one ahead of them ----
       QbUnit u = qb_locate<N>(a, first, lane), ahead;
       long long left = n_tiles;
@@ -1061,9 +1032,9 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       if (!ok)  // no copy in flight when the CTA ends
         for (int k = max(0, i - QB_STAGES); k < i; ++k) mbar_wait_bounded(&sh.full[k % QB_STAGES], (k / QB_STAGES) & 1);
     } else if (warp > 17) {
-      if constexpr (N == 64) qb_registers<56, false>();
+      if constexpr (N == 64) qb_registers<40, false>();
     } else {
-      if constexpr (N == 64) qb_registers<56, false>();
+      if constexpr (N == 64) qb_registers<40, false>();
       // ---- MMA issue ----
       constexpr uint32_t I_QK = qb_idesc(N, false), I_PV = qb_idesc(N, true);
       auto pv = [&](int i) {
