@@ -466,6 +466,16 @@ __device__ __forceinline__ uint32_t qb_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // A token's constants: key scale and zero, log2 of the value scale, its reciprocal, value mid over value scale.
+// A vote of four warps at hardware barrier `id`.
+__device__ __forceinline__ bool qb_vote(int id, bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any)
+      : "r"((uint32_t)p), "r"(id)
+      : "memory");
+  return any != 0;
+}
 enum { QB_C_SK, QB_C_KZ, QB_C_LS, QB_C_INV, QB_C_ZC };
 
 // Register shares of a group of four warps (the block's total stays what it was launched with).
@@ -482,7 +492,6 @@ struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) float neg_m[N];       // -M of the running unit
   alignas(16) float scale[4][N];    // factors of the accumulated numerator for tile i (i % 4), where flagged
   alignas(8) int moved[4][2];       // per half of the rows: whether tile i (i % 4) moved a reference
-  alignas(16) int vote[2][2][4];    // per half of the softmax warps: the warps' votes, two rounds
   alignas(16) int red[2][4][32];    // per half: the rows' maxima per warp
   alignas(16) float delta[2][32];   // per half: how far the references moved
   alignas(16) float tok[4][5][QB_TOK];  // constants of tile i (i % 4): see QB_C_*
@@ -502,7 +511,7 @@ struct QbShared {  // alignas: read as 16-byte vectors
   uint64_t group[3];                // meetings of the four warps of a softmax half (0, 1) and of the accumulation (2)
   uint32_t tmem;
 };
-static_assert(offsetof(QbShared<16>, neg_m) % 16 == 0 && offsetof(QbShared<16>, vote) % 16 == 0 &&
+static_assert(offsetof(QbShared<16>, neg_m) % 16 == 0 && offsetof(QbShared<16>, tok) % 16 == 0 &&
                   offsetof(QbShared<16>, scale) % 16 == 0 && offsetof(QbShared<16>, sumq) % 16 == 0,
               "vector reads");
 
@@ -672,43 +681,58 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       const int tok = 32 * q4 + lane;
       const bool lead = tid == 128 + 128 * half;
-      int i = 0;
+      float unscale = 0.f;
+      const float* s_sumq = nullptr;
+      const int* s_tin = nullptr;
+      int un = -1, t = 0, t1 = 0, base = 0, open = 0, len = 0, c0 = 0;
+      bool unset = false;
+      uint64_t l2[NH / 2], z2[NH / 2];
+      // One hardware vote a tile, so every warp makes exactly n_tiles rounds: one whose wait has run out
+      // stays in step with the others and does nothing else.
       bool ok = true;
-      for (int un = 0; ok; ++un) {
-        if (!wait(&sh.unit_full[un % QB_UNITS], un / QB_UNITS)) break;
-        const QbUnit u = sh.unit[un % QB_UNITS];
-        arrive(&sh.unit_free[un % QB_UNITS]);
-        if (u.t1 == u.t0) break;
-        if (!wait(&sh.q_ready[un & 1], un >> 1)) break;
-        const float unscale = sh.unscale[un & 1];
-        const float* s_sumq = sh.sumq[un & 1];
-        const int* s_tin = sh.tin[un & 1];
-        const int base = a.mode == QB_CROSS ? u.len : u.len - u.n;
-        // positions below `open` are seen by every row of the tile
-        const int open = a.mode == QB_CHAIN ? base + u.rt * (N >> a.gqa_shift) + 1 : base;
-        if (!meet(half)) break;  // the last unit's references are no longer read
-        if (tok < NH) sh.neg_m[col0 + tok] = 0.f;
-        bool unset = tok < NH;  // row col0 + tok has seen nothing yet, and M = 0
-        if (!meet(half)) break;
-        uint64_t l2[NH / 2], z2[NH / 2];
+      for (int i = 0; i < n_tiles; ++i, ++t) {
+        const int buf = i & 1, use = i >> 1;
+        if (t == t1 && ok) {
+          ++un;
+          if ((ok = wait(&sh.unit_full[un % QB_UNITS], un / QB_UNITS) && wait(&sh.q_ready[un & 1], un >> 1) && meet(half))) {
+            const QbUnit& u = sh.unit[un % QB_UNITS];
+            t = u.t0;
+            t1 = u.t1;
+            len = u.len;
+            c0 = u.c0;
+            base = a.mode == QB_CROSS ? u.len : u.len - u.n;
+            // positions below `open` are seen by every row of the tile
+            open = a.mode == QB_CHAIN ? base + u.rt * (N >> a.gqa_shift) + 1 : base;
+            arrive(&sh.unit_free[un % QB_UNITS]);
+            unscale = sh.unscale[un & 1];
+            s_sumq = sh.sumq[un & 1];
+            s_tin = sh.tin[un & 1];
+            if (tok < NH) sh.neg_m[col0 + tok] = 0.f;
+            unset = tok < NH;  // row col0 + tok has seen nothing yet, and M = 0
+            ok = meet(half);
 #pragma unroll
-        for (int j = 0; j < NH / 2; ++j) l2[j] = z2[j] = 0ull;
-        for (int t = u.t0; t < u.t1; ++t, ++i) {
-          const int buf = i & 1, use = i >> 1;
+            for (int j = 0; j < NH / 2; ++j) l2[j] = z2[j] = 0ull;
+          }
+        }
+        {
           const bool masked = (t + 1) * QB_TOK > open;
           int key_tin = 0;
           unsigned key_size = 0x7fffffffu;
-          if (__builtin_expect(masked, 0)) {
+          if (__builtin_expect(masked && ok, 0)) {
             const int d = t * QB_TOK + tok - base;
-            if (d + base >= u.len) {
+            if (d + base >= len) {
               key_size = 0u;
             } else if (d >= 0) {
-              const int2 ts = a.mode == QB_TREE ? a.ws.tree[u.c0 + d] : make_int2(d, u.n - d);
+              const int2 ts = a.mode == QB_TREE ? a.ws.tree[c0 + d] : make_int2(d, len - base - d);
               key_tin = ts.x;
               key_size = (unsigned)ts.y;
             }
           }
-          if (!(ok = wait(&sh.s_done[buf], use))) break;
+          if (!ok || !wait(&sh.s_done[buf], use)) {
+            ok = false;
+            qb_vote(1 + half, false);
+            continue;
+          }
           tc_fence_after();
           const float(*tc)[QB_TOK] = sh.tok[i & 3];
           const float sk = tc[QB_C_SK][tok] * unscale, kz = tc[QB_C_KZ][tok], ls = tc[QB_C_LS][tok],
@@ -740,16 +764,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           float top = -INFINITY;
 #pragma unroll
           for (int j = 0; j < NH; j += 2) top = qb_max3(top, x[j], x[j + 1]);
-          // whether any weight of the 128 tokens passes the limit: voted on while the weights are taken
-          const bool mine = __any_sync(FULLM, top > QB_TRIGGER || unset);
-          int* votes = sh.vote[half][round & 1];
-          if (lane == 0) votes[q4] = mine;
-          arrive(&sh.group[half]);
+          // whether any weight of the 128 tokens would pass the limit
+          const bool move = qb_vote(1 + half, top > QB_TRIGGER || unset);
 #pragma unroll
           for (int j = 0; j < NH; ++j) x[j] = qb_ex2(x[j]);
-          if (!(ok = wait(&sh.group[half], round++))) break;
-          const int4 v4 = *reinterpret_cast<const int4*>(votes);
-          const bool move = (v4.x | v4.y | v4.z | v4.w) != 0;
           if (lead) sh.moved[i & 3][half] = move;
           if (__builtin_expect(move, 0)) {
             // the references move up to the rows' maxima over the 128 tokens
@@ -761,7 +779,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
               if (lane == j) row_max = m;
             }
             if (lane < NH) sh.red[half][q4][lane] = row_max;
-            if (!(ok = meet(half))) break;
+            if (!(ok = meet(half))) continue;
             if (tok < NH) {
               const float m = qb_unordered(max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
                                                max(sh.red[half][2][tok], sh.red[half][3][tok])));
@@ -771,7 +789,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
               sh.scale[i & 3][col0 + tok] = unset ? 1.f : qb_ex2(-by);  // nothing to scale yet
               if (m > -INFINITY) unset = false;
             }
-            if (!(ok = meet(half))) break;
+            if (!(ok = meet(half))) continue;
 #pragma unroll
             for (int j = 0; j < NH; j += 2) {
               const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col0 + j);
@@ -785,7 +803,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
           tc_fence_before();  // the scores are in registers
           arrive(&sh.s_free[buf]);
-          if (use && !(ok = wait(&sh.o_done[buf], use - 1))) break;
+          if (use && !(ok = wait(&sh.o_done[buf], use - 1))) continue;
 #pragma unroll
           for (int j = 0; j < NH; j += 8) {  // two fp16 halves of every weight
             uint32_t hi[4], lo[4];
@@ -810,7 +828,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             z2[j / 2] = f2fma(w2, zc2, z2[j / 2]);
           }
         }
-        if (!ok) break;
+        if (t + 1 < t1) continue;
         // the unit's l and sum p mid: over the warp's 32 tokens by exchange and halving, over the warps by the writer
         float l[NH], z[NH];
 #pragma unroll
@@ -841,7 +859,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             z[0] += __shfl_xor_sync(FULLM, z[0], d);
           }
         }
-        if (un && !wait(&sh.lz_free, un - 1)) break;
+        if (un && !(ok = wait(&sh.lz_free, un - 1))) continue;
         if ((lane & (32 / NH - 1)) == 0) {
           sh.lsum[q4][col0 + cols] = l[0];
           sh.zsum[q4][col0 + cols] = z[0];
@@ -1037,40 +1055,24 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       if constexpr (N == 64) qb_registers<40, false>();
       // ---- MMA issue ----
       constexpr uint32_t I_QK = qb_idesc(N, false), I_PV = qb_idesc(N, true);
-      auto pv = [&](int i) {
-        const int buf = i & 1, use = i >> 1;
-        if (!wait(&sh.v_ready[buf], use) || !wait(&sh.p_ready[buf], use) || (use && !wait(&sh.o_free[buf], use - 1)))
-          return false;
-        tc_fence_after();
-        if (qb_elect()) {
-          const uint64_t hi = sw128_desc(s_p + (2 * buf) * QB_PBUF), lo = sw128_desc(s_p + (2 * buf + 1) * QB_PBUF);
-          const uint32_t av = tmem + T_V + 64 * buf, d = tmem + T_O + 64 * buf;
-          // loops on purpose: the roles' code has to fit the instruction cache together
-#pragma unroll 1
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, av + 8 * k, (p ? hi : lo) + k * (2048 >> 4), I_PV, p + k > 0);
-          tc_commit(&sh.o_done[buf]);
-        }
-        __syncwarp();
-        return true;
-      };
-      int i = 0;
+      int un = -1, left = 0;
+      uint64_t q = 0;
       bool ok = true;
-      for (int un = 0; ok; ++un) {
-        if (!(ok = wait(&sh.unit_full[un % QB_UNITS], un / QB_UNITS))) break;
-        const int count = sh.unit[un % QB_UNITS].t1 - sh.unit[un % QB_UNITS].t0;
-        arrive(&sh.unit_free[un % QB_UNITS]);
-        if (count == 0) break;
-        if (!(ok = wait(&sh.q_ready[un & 1], un >> 1))) break;
-        const uint8_t* qt = s_q + (un & 1) * N * 512;
-        for (int t = 0; t < count; ++t, ++i) {
+      for (int i = 0; i <= n_tiles; ++i) {  // the scores of tile i, then the readout of tile i - 1
+        if (i < n_tiles) {
           const int buf = i & 1, use = i >> 1;
+          if (left == 0) {
+            ++un;
+            if (!(ok = wait(&sh.unit_full[un % QB_UNITS], un / QB_UNITS) && wait(&sh.q_ready[un & 1], un >> 1))) break;
+            left = sh.unit[un % QB_UNITS].t1 - sh.unit[un % QB_UNITS].t0;
+            arrive(&sh.unit_free[un % QB_UNITS]);
+            q = sw128_desc(s_q + (un & 1) * N * 512);
+          }
+          --left;
           if (!(ok = wait(&sh.k_ready[buf], use) && (!use || wait(&sh.s_free[buf], use - 1)))) break;
           tc_fence_after();
           if (qb_elect()) {
             const uint32_t ak = tmem + T_K + 64 * buf, d = tmem + T_S + 64 * buf;
-            const uint64_t q = sw128_desc(qt);
 #pragma unroll 1
             for (int p = 0; p < 2; ++p)  // lo, then hi: 4 steps of 16 channels in each of two halves
 #pragma unroll
@@ -1079,10 +1081,25 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             tc_commit(&sh.s_done[buf]);
           }
           __syncwarp();
-          if (i > 0 && !(ok = pv(i - 1))) break;
+        }
+        if (i > 0) {
+          const int buf = (i - 1) & 1, use = (i - 1) >> 1;
+          if (!(ok = wait(&sh.v_ready[buf], use) && wait(&sh.p_ready[buf], use) &&
+                     (!use || wait(&sh.o_free[buf], use - 1))))
+            break;
+          tc_fence_after();
+          if (qb_elect()) {
+            const uint64_t hi = sw128_desc(s_p + (2 * buf) * QB_PBUF), lo = sw128_desc(s_p + (2 * buf + 1) * QB_PBUF);
+            const uint32_t av = tmem + T_V + 64 * buf, d = tmem + T_O + 64 * buf;
+#pragma unroll 1
+            for (int p = 0; p < 2; ++p)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, av + 8 * k, (p ? hi : lo) + k * (2048 >> 4), I_PV, p + k > 0);
+            tc_commit(&sh.o_done[buf]);
+          }
+          __syncwarp();
         }
       }
-      if (ok) ok = pv(i - 1);
       if (!ok) {  // let the tensor cores finish before their memory is freed
         if (qb_elect()) tc_commit(&sh.last);
         __syncwarp();
