@@ -27,8 +27,8 @@
 // Softmax weights are kept as w = 2^(a + log2 s - M) directly, p = w / s: fp16 then
 // holds w whatever the value scales are (a constant group, s = 0, takes the
 // smallest fp16 as s: its codes are 0 and mid compensates exactly).  M is a lazy
-// reference, 2^8 below a running maximum and moved only when a weight would pass
-// 2^14: one vote a tile, and most tiles never move it.
+// reference, the maximum of the first tile, moved only when a weight would pass
+// 2^14: one vote a tile, and most units never move it again.
 //
 // A CTA (18 warps, one per SM, persistent over an equal slice of all tiles):
 //   warps 0-3    expand the codes of a tile into tensor memory: a thread owns a token
@@ -56,7 +56,7 @@ constexpr int QB_STAGE_BYTES = QB_TOK * 72;
 constexpr int QB_THREADS = 20 * 32;                // 18 warps work; register shares go by groups of four warps
 constexpr int QB_PBUF = QB_TOK * 128;             // one half of W^T: 128 rows of 128 bytes (64 fp16 columns)
 constexpr int QB_UNITS = 4;                       // ring of unit descriptors
-constexpr float QB_LIFT = 8.f, QB_TRIGGER = 14.f; // weights: running maximum at 2^8, moved when one would pass 2^14
+constexpr float QB_TRIGGER = 14.f;                // the reference moves to the running maximum when a weight would pass 2^14
 
 __host__ __device__ constexpr int qb_smem_bytes(int n) {
   return 1024 + 2 * n * 512 + 2 * 2 * QB_PBUF + QB_STAGES * QB_STAGE_BYTES + n * D * 4;
@@ -493,7 +493,7 @@ struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) float scale[4][N];    // factors of the accumulated numerator for tile i (i % 4), where flagged
   alignas(8) int moved[4][2];       // per half of the rows: whether tile i (i % 4) moved a reference
   alignas(16) int red[2][4][32];    // per half: the rows' maxima per warp
-  alignas(16) float delta[2][32];   // per half: how far the references moved
+  int fresh[2];                     // per half: whether a row has seen nothing yet
   alignas(16) float tok[4][5][QB_TOK];  // constants of tile i (i % 4): see QB_C_*
   alignas(16) float lsum[4][N];
   alignas(16) float zsum[4][N];
@@ -685,7 +685,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       const float* s_sumq = nullptr;
       const int* s_tin = nullptr;
       int un = -1, t = 0, t1 = 0, base = 0, open = 0, len = 0, c0 = 0;
-      bool unset = false;
+      bool unset = false, fresh = false;
       uint64_t l2[NH / 2], z2[NH / 2];
       // One hardware vote a tile, so every warp makes exactly n_tiles rounds: one whose wait has run out
       // stays in step with the others and does nothing else.
@@ -709,6 +709,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             s_tin = sh.tin[un & 1];
             if (tok < NH) sh.neg_m[col0 + tok] = 0.f;
             unset = tok < NH;  // row col0 + tok has seen nothing yet, and M = 0
+            fresh = true;      // some row has not
             ok = meet(half);
 #pragma unroll
             for (int j = 0; j < NH / 2; ++j) l2[j] = z2[j] = 0ull;
@@ -740,11 +741,56 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           const uint64_t sk2 = f2pk(sk, sk), kz2 = f2pk(kz, kz), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
                          zc2 = f2pk(zc, zc);
           uint8_t* p_hi = s_p + (2 * buf) * QB_PBUF + tok * 128;
-          float x[NH];
-          auto logits = [&]() {  // x: a + log2 s - M, -infinity where the row does not see the token
+          const uint32_t scores = tmem + lanes + T_S + 64 * buf + col0;
+          // the references move up to the rows' maxima over the 128 tokens (rare: a short loop, off the common path)
+          auto move_references = [&]() {
+            int row_max = 0;
+#pragma unroll 1
+            for (int j = 0; j < NH; j += 8) {
+              float v[8];
+              tmem_ld8(scores + j, v);
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-              qb_tmem_ld<CH>(tmem + lanes + T_S + 64 * buf + col0 + c * CH, *reinterpret_cast<float(*)[CH]>(x + c * CH));
+              for (int k = 0; k < 8; ++k) {
+                const int col = col0 + j + k;
+                v[k] = fmaf(sk, v[k], fmaf(kz, s_sumq[col], sh.neg_m[col] + ls));
+                if ((unsigned)(s_tin[col] - key_tin) >= key_size) v[k] = -INFINITY;
+                const int m = __reduce_max_sync(FULLM, qb_ordered(v[k]));
+                if (lane == j + k) row_max = m;
+              }
+            }
+            if (lane < NH) sh.red[half][q4][lane] = row_max;
+            if (!meet(half)) return false;
+            if (q4 == 0) {
+              if (tok < NH) {
+                const float m = qb_unordered(max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
+                                                 max(sh.red[half][2][tok], sh.red[half][3][tok])));
+                const float by = (unset ? m > -INFINITY : m > 0.f) ? m : 0.f;
+                sh.neg_m[col0 + tok] -= by;
+                sh.scale[i & 3][col0 + tok] = unset ? 1.f : qb_ex2(-by);  // nothing to scale yet
+                if (m > -INFINITY) unset = false;
+              }
+              const bool some = __any_sync(FULLM, unset);
+              if (lane == 0) {
+                sh.fresh[half] = some;
+                sh.moved[i & 3][half] = 1;
+              }
+            }
+            if (!meet(half)) return false;
+            fresh = sh.fresh[half] != 0;
+#pragma unroll
+            for (int j = 0; j < NH; j += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col0 + j);
+              const uint64_t f2 = f2pk(f.x, f.y);
+              l2[j / 2] = f2mul(l2[j / 2], f2);
+              z2[j / 2] = f2mul(z2[j / 2], f2);
+            }
+            return true;
+          };
+          if (lead) sh.moved[i & 3][half] = 0;
+          float x[NH], top;
+          auto logits = [&]() {  // x: a + log2 s - M, -infinity where the row does not see the token; top: the largest
+#pragma unroll
+            for (int c = 0; c < NC; ++c) qb_tmem_ld<CH>(scores + c * CH, *reinterpret_cast<float(*)[CH]>(x + c * CH));
 #pragma unroll
             for (int j = 0; j < NH; j += 4) {
               const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col0 + j);
@@ -759,47 +805,20 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
 #pragma unroll
               for (int j = 0; j < NH; ++j) x[j] = (unsigned)(s_tin[col0 + j] - key_tin) < key_size ? x[j] : -INFINITY;
             }
+            top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < NH; j += 2) top = qb_max3(top, x[j], x[j + 1]);
           };
           logits();
-          float top = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < NH; j += 2) top = qb_max3(top, x[j], x[j + 1]);
           // whether any weight of the 128 tokens would pass the limit
-          const bool move = qb_vote(1 + half, top > QB_TRIGGER || unset);
+          const bool move = qb_vote(1 + half, top > QB_TRIGGER || fresh);
 #pragma unroll
           for (int j = 0; j < NH; ++j) x[j] = qb_ex2(x[j]);
-          if (lead) sh.moved[i & 3][half] = move;
           if (__builtin_expect(move, 0)) {
-            // the references move up to the rows' maxima over the 128 tokens
+            if (!(ok = move_references())) continue;
             logits();
-            int row_max = 0;
 #pragma unroll
-            for (int j = 0; j < NH; ++j) {
-              const int m = __reduce_max_sync(FULLM, qb_ordered(x[j]));
-              if (lane == j) row_max = m;
-            }
-            if (lane < NH) sh.red[half][q4][lane] = row_max;
-            if (!(ok = meet(half))) continue;
-            if (tok < NH) {
-              const float m = qb_unordered(max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
-                                               max(sh.red[half][2][tok], sh.red[half][3][tok])));
-              const float by = (unset ? m > -INFINITY : m > QB_LIFT) ? m - QB_LIFT : 0.f;
-              sh.neg_m[col0 + tok] -= by;
-              sh.delta[half][tok] = by;
-              sh.scale[i & 3][col0 + tok] = unset ? 1.f : qb_ex2(-by);  // nothing to scale yet
-              if (m > -INFINITY) unset = false;
-            }
-            if (!(ok = meet(half))) continue;
-#pragma unroll
-            for (int j = 0; j < NH; j += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col0 + j);
-              const float2 by = *reinterpret_cast<const float2*>(sh.delta[half] + j);
-              const uint64_t f2 = f2pk(f.x, f.y);
-              l2[j / 2] = f2mul(l2[j / 2], f2);
-              z2[j / 2] = f2mul(z2[j / 2], f2);
-              x[j] = qb_ex2(x[j] - by.x);
-              x[j + 1] = qb_ex2(x[j + 1] - by.y);
-            }
+            for (int j = 0; j < NH; ++j) x[j] = qb_ex2(x[j]);
           }
           tc_fence_before();  // the scores are in registers
           arrive(&sh.s_free[buf]);
@@ -829,41 +848,31 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
         }
         if (t + 1 < t1) continue;
-        // the unit's l and sum p mid: over the warp's 32 tokens by exchange and halving, over the warps by the writer
-        float l[NH], z[NH];
+        // the unit's l and sum p mid over the 128 tokens: every thread leaves its NH values where its weights of the
+        // next tile will go, and adds one row up over 32 tokens
+        if ((i > 0 && !(ok = wait(&sh.o_done[(i - 1) & 1], (i - 1) >> 1))) || (un && !(ok = wait(&sh.lz_free, un - 1))))
+          continue;
+        uint8_t* mine = s_p + 2 * ((i + 1) & 1) * QB_PBUF;
+        auto at = [&](int row, int token) {  // two 8-row chunks' places (hi and lo) hold 8 rows of fp32
+          return mine + ((row >> 2) & 1) * QB_PBUF + token * 128 + ((((col0 + row) >> 3) ^ (token & 7)) << 4);
+        };
 #pragma unroll
-        for (int j = 0; j < NH / 2; ++j) {
-          const float2 p = f2up(l2[j]), q = f2up(z2[j]);
-          l[2 * j] = p.x; l[2 * j + 1] = p.y;
-          z[2 * j] = q.x; z[2 * j + 1] = q.y;
-        }
-        int cols = 0;  // column this lane ends up with
-        int width = NH;
+        for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) {
-          if (d >= 32 / NH * 1 && width > 1) {
-            width >>= 1;
-            const bool up = lane & d;
-#pragma unroll
-            for (int j = 0; j < NH / 2; ++j) {
-              if (j < width) {
-                const float sl = up ? l[j] : l[j + width], sz = up ? z[j] : z[j + width];
-                const float kl = up ? l[j + width] : l[j], kz = up ? z[j + width] : z[j];
-                l[j] = kl + __shfl_xor_sync(FULLM, sl, d);
-                z[j] = kz + __shfl_xor_sync(FULLM, sz, d);
-              }
-            }
-            if (up) cols += width;
-          } else {
-            l[0] += __shfl_xor_sync(FULLM, l[0], d);
-            z[0] += __shfl_xor_sync(FULLM, z[0], d);
+          for (int j = 0; j < NH; j += 4) {
+            const float2 p = f2up(pass ? z2[j / 2] : l2[j / 2]), q = f2up(pass ? z2[j / 2 + 1] : l2[j / 2 + 1]);
+            *reinterpret_cast<float4*>(at(j, tok)) = make_float4(p.x, p.y, q.x, q.y);
           }
+          if (!(ok = meet(half))) break;
+          if (lane < NH) {
+            float sum = 0.f;
+#pragma unroll 2
+            for (int k = 0; k < 32; ++k) sum += reinterpret_cast<const float*>(at(lane, 32 * q4 + k))[lane & 3];
+            (pass ? sh.zsum : sh.lsum)[q4][col0 + lane] = sum;
+          }
+          if (!(ok = meet(half))) break;
         }
-        if (un && !(ok = wait(&sh.lz_free, un - 1))) continue;
-        if ((lane & (32 / NH - 1)) == 0) {
-          sh.lsum[q4][col0 + cols] = l[0];
-          sh.zsum[q4][col0 + cols] = z[0];
-        }
+        if (!ok) continue;
         if (tok < NH) sh.m_out[col0 + tok] = -sh.neg_m[col0 + tok];
         arrive(&sh.lz_ready);
       }
@@ -888,7 +897,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           const float* src =
               a.ws.q + ((size_t)(next.c0 + (valid ? tk : 0)) * a.n_q_heads + next.h * a.gqa + (R & gm)) * D + part * N;
           float m = 0.f, s = 0.f;
-#pragma unroll 4
+#pragma unroll 2
           for (int j = 0; j < N; j += 4) {
             const float4 v = valid ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
             s += (v.x + v.y) + (v.z + v.w);
