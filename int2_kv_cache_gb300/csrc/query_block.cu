@@ -41,6 +41,7 @@
 // A unit is (sequence, KV head, row tile).  Slices cut units: a unit wholly inside a
 // CTA is written out at once, a cut one leaves partials (numerator, l, M) that
 // qb_combine_kernel joins in slice order (results do not depend on timing).
+#include <algorithm>
 #include <cstddef>
 
 #include "quant_common.cuh"
@@ -240,7 +241,7 @@ __device__ __forceinline__ void qb_next(const QbArgs& a, QbUnit& u) {
 
 // ---------------------------------------------------------------------------
 // Preparation: one launch for the list of tiles (block 0), the trees' numbering (one
-// block a sequence) and the rotation of the queries (a warp a row).
+// block a sequence) and the rotation of the queries.
 // ---------------------------------------------------------------------------
 constexpr int QB_PREP_THREADS = 256;
 
@@ -269,8 +270,9 @@ __device__ __forceinline__ void qb_list_tiles(const QbArgs& a) {
   if (threadIdx.x == QB_PREP_THREADS - 1) a.ws.tiles[a.n_seqs] = at;
 }
 
-__device__ __forceinline__ void qb_number_tree(const QbArgs& a, int b, const int32_t* __restrict__ parents) {
-  __shared__ int s_par[QB_MAX_TREE], s_size[QB_MAX_TREE], s_off[QB_MAX_TREE];
+__device__ __forceinline__ void qb_number_tree(const QbArgs& a, int b, const int32_t* __restrict__ parents,
+                                               int* smem) {
+  int *s_par = smem, *s_size = smem + QB_MAX_TREE, *s_off = smem + 2 * QB_MAX_TREE;
   const QbSeq q = qb_seq(a, b, nullptr);
   for (int i = threadIdx.x; i < q.n; i += blockDim.x) {
     int p = parents[q.c0 + i];
@@ -300,9 +302,9 @@ __device__ __forceinline__ void qb_number_tree(const QbArgs& a, int b, const int
   }
 }
 
-// One warp a row (token, query head): y = x R * scale.
+// Identity and signed Hadamard, one warp a row (token, query head): y = x R * scale.
 __device__ __forceinline__ void qb_rotate_row(const QbArgs& a, long long r, const void* __restrict__ q, int dtype,
-                                              const RotDev& rot, float* s_x, int lane) {
+                                              const RotDev& rot, int lane) {
   const int h = (int)(r % a.n_q_heads) / a.gqa;
   const float4 x = load4(q, (size_t)r * D + 4 * lane, dtype);
   float y[4] = {x.x, x.y, x.z, x.w};
@@ -320,36 +322,118 @@ __device__ __forceinline__ void qb_rotate_row(const QbArgs& a, long long r, cons
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] *= 0.08838834764831845f;
-  } else if (rot.kind == KVQ_ROT_DENSE) {
-    *reinterpret_cast<float4*>(s_x + 4 * lane) = x;
-    __syncwarp();
-    y[0] = y[1] = y[2] = y[3] = 0.f;
-    const float* R = rot.dense + (size_t)h * D * D;
-#pragma unroll 8
-    for (int c = 0; c < D; ++c) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(R + c * D + 4 * lane));
-      const float v = s_x[c];
-      y[0] = fmaf(v, w.x, y[0]); y[1] = fmaf(v, w.y, y[1]); y[2] = fmaf(v, w.z, y[2]); y[3] = fmaf(v, w.w, y[3]);
-    }
   }
   *reinterpret_cast<float4*>(a.ws.q + (size_t)r * D + 4 * lane) =
       make_float4(y[0] * QB_SCALE, y[1] * QB_SCALE, y[2] * QB_SCALE, y[3] * QB_SCALE);
 }
 
+// Dense rotations: a block takes 32 columns of one KV head's R and every `chunks`-th tile of
+// 64 of its rows.  fp32 values are split into three bf16 limbs (24 bits, exact), bf16 queries
+// are one; the products whose limbs count from 2^0 to 2^-16 are taken on mma.sync (m16n8k16,
+// fp32 accumulation), 3 for bf16 queries and 6 for fp32, smallest first: about 2^-22 relative.
+// The rotation is a few per cent of the attention's work, so it needs no tensor memory.
+constexpr int QB_ROT_ROWS = 64, QB_ROT_COLS = 32;
+
+__device__ __forceinline__ void qb_split3(float x, float y, uint32_t (&limb)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    limb[i] = *reinterpret_cast<const uint32_t*>(&h);
+    x -= __low2float(h);
+    y -= __high2float(h);
+  }
+}
+
+__device__ __forceinline__ void qb_mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+
+template <bool F32>
+__device__ __forceinline__ void qb_rotate_dense(const QbArgs& a, int h, int slice, int chunk, int chunks,
+                                                const void* __restrict__ q, const float* __restrict__ dense,
+                                                uint2 (*s_b)[8][QB_ROT_COLS / 8][32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // R's limbs as B fragments: [limb][16-channel step][8 columns][lane = 4 (column % 8) + pair]
+  for (int p = warp; p < 64; p += QB_PREP_THREADS / 32) {  // channels 2p, 2p + 1; a lane a column
+    const float* r = dense + ((size_t)h * D + 2 * p) * D + QB_ROT_COLS * slice + lane;
+    uint32_t limb[3];
+    qb_split3(__ldg(r), __ldg(r + D), limb);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      reinterpret_cast<uint32_t*>(&s_b[i][p >> 3][lane >> 3][4 * (lane & 7) + (p & 3)])[(p >> 2) & 1] = limb[i];
+  }
+  __syncthreads();
+  const int rows = a.n_total << a.gqa_shift, gm = a.gqa - 1;  // n_total * n_q_heads < 2^31
+  const int rg = warp & 3, cg = warp >> 2, g = lane >> 2, t = lane & 3;
+  auto offset = [&](int r) { return ((size_t)(r >> a.gqa_shift) * a.n_q_heads + h * a.gqa + (r & gm)) * D; };
+  for (long long r0 = (long long)chunk * QB_ROT_ROWS; r0 < rows; r0 += (long long)chunks * QB_ROT_ROWS) {
+    const int ra = (int)r0 + 16 * rg + g, rb = ra + 8;
+    const size_t oa = offset(min(ra, rows - 1)), ob = offset(min(rb, rows - 1));
+    float d[2][4] = {};
+#pragma unroll 2
+    for (int k = 0; k < 8; ++k) {
+      uint32_t x[F32 ? 3 : 1][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // rows g, g + 8; channels 2t, 2t + 1 and 8 further
+        const size_t at = ((i & 1) ? ob : oa) + 16 * k + 2 * t + 8 * (i >> 1);
+        if constexpr (F32) {
+          const float2 v = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(q) + at));
+          uint32_t limb[3];
+          qb_split3(v.x, v.y, limb);
+          x[0][i] = limb[0]; x[1][i] = limb[1]; x[2][i] = limb[2];
+        } else {
+          x[0][i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(q) + at));
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint2 b[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) b[i] = s_b[i][k][2 * cg + n][lane];
+        if constexpr (F32) {
+          qb_mma_bf16(d[n], x[2], b[0]);
+          qb_mma_bf16(d[n], x[1], b[1]);
+          qb_mma_bf16(d[n], x[0], b[2]);
+          qb_mma_bf16(d[n], x[1], b[0]);
+        } else {
+          qb_mma_bf16(d[n], x[0], b[2]);
+        }
+        qb_mma_bf16(d[n], x[0], b[1]);
+        qb_mma_bf16(d[n], x[0], b[0]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int col = QB_ROT_COLS * slice + 16 * cg + 8 * n + 2 * t;
+      if (ra < rows)
+        *reinterpret_cast<float2*>(a.ws.q + oa + col) = make_float2(d[n][0] * QB_SCALE, d[n][1] * QB_SCALE);
+      if (rb < rows)
+        *reinterpret_cast<float2*>(a.ws.q + ob + col) = make_float2(d[n][2] * QB_SCALE, d[n][3] * QB_SCALE);
+    }
+  }
+}
+
 template <int N>
 __global__ void __launch_bounds__(QB_PREP_THREADS)
-qb_prepare_kernel(QbArgs a, const int32_t* __restrict__ parents, const void* __restrict__ q, int dtype, RotDev rot) {
-  __shared__ __align__(16) float s_x[QB_PREP_THREADS / 32][D];
+qb_prepare_kernel(QbArgs a, const int32_t* __restrict__ parents, const void* __restrict__ q, int dtype, RotDev rot,
+                  int chunks) {
+  __shared__ __align__(16) uint2 s_b[3][8][QB_ROT_COLS / 8][32];
   pdl_launch_dependents();
   const int trees = a.mode == QB_TREE ? a.n_seqs : 0;
+  const int block = (int)blockIdx.x - 1 - trees;
   if (blockIdx.x == 0) {
     qb_list_tiles<N>(a);
-  } else if ((int)blockIdx.x <= trees) {
-    qb_number_tree(a, blockIdx.x - 1, parents);
+  } else if (block < 0) {
+    qb_number_tree(a, blockIdx.x - 1, parents, reinterpret_cast<int*>(s_b));
+  } else if (rot.kind == KVQ_ROT_DENSE) {
+    const int H = a.g.n_kv_heads, h = block % H, slice = block / H % (D / QB_ROT_COLS), chunk = block / (H * (D / QB_ROT_COLS));
+    if (dtype == KVQ_F32) qb_rotate_dense<true>(a, h, slice, chunk, chunks, q, rot.dense, s_b);
+    else qb_rotate_dense<false>(a, h, slice, chunk, chunks, q, rot.dense, s_b);
   } else {
-    const long long r = (long long)(blockIdx.x - 1 - trees) * (QB_PREP_THREADS / 32) + (threadIdx.x >> 5);
-    if (r < (long long)a.n_total * a.n_q_heads)
-      qb_rotate_row(a, r, q, dtype, rot, s_x[threadIdx.x >> 5], threadIdx.x & 31);
+    const long long r = (long long)block * (QB_PREP_THREADS / 32) + (threadIdx.x >> 5);
+    if (r < (long long)a.n_total * a.n_q_heads) qb_rotate_row(a, r, q, dtype, rot, threadIdx.x & 31);
   }
 }
 
@@ -1126,55 +1210,53 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
 
 // Units cut by slices.  Block k joins the unit that starts in slice k and runs past its
 // end: its partial there (slot 2k + 1) and slots 2j of the following slices, in order.
-constexpr int QB_JOIN_ROWS = 8;
+constexpr int QB_JOIN_ROWS = 8;  // a warp a row
 
 template <int N>
-__global__ void __launch_bounds__(D) qb_combine_kernel(QbArgs a, int grid) {
-  __shared__ QbUnit s_u;
-  __shared__ long long s_u0;
-  pdl_wait();
+__global__ void __launch_bounds__(32 * QB_JOIN_ROWS) qb_combine_kernel(QbArgs a, int grid) {
+  const int lane = threadIdx.x & 31, r = blockIdx.y * QB_JOIN_ROWS + (threadIdx.x >> 5);
+  // the list of tiles is complete: the attention's blocks waited for it before they let this grid start
   const long long total = a.ws.tiles[a.n_seqs];
   const QbSlices slices(total, grid);
   const int k = blockIdx.x;
   const long long start = slices.start(k), end = slices.start(k + 1);
-  if (end == start) return;
-  if (threadIdx.x < 32) {
-    const QbUnit u = qb_locate<N>(a, end - 1, threadIdx.x);
-    if (threadIdx.x == 0) {
-      s_u = u;
-      s_u0 = end - 1 - u.t0;
-    }
+  if (end == start) {
+    pdl_wait();  // every block ends after the attention, so that what follows this grid does too
+    return;
   }
-  __syncthreads();
-  const QbUnit u = s_u;
-  const long long u0 = s_u0, u1 = u0 + u.nt;
-  if (u1 <= end || u0 < start) return;
+  const QbUnit u = qb_locate<N>(a, end - 1, lane);
+  const long long u0 = end - 1 - u.t0, u1 = u0 + u.nt;
+  const int R = u.rt * N + r, tk = R >> a.gqa_shift;
+  if (u1 <= end || u0 < start || tk >= u.n) {
+    pdl_wait();
+    return;
+  }
   int parts = 1;  // slices after k are not empty before u1: sizes differ by one, larger ones first
   while (slices.start(k + parts) < u1) ++parts;
   const float* first = a.ws.part + (size_t)(2 * k + 1) * N * (D + 2);
   const float* rest = a.ws.part + (size_t)(2 * k) * N * (D + 2);  // + 2 j slots: slice k + j
   const size_t step = (size_t)2 * N * (D + 2);
-  for (int r = blockIdx.y * QB_JOIN_ROWS; r < (int)(blockIdx.y + 1) * QB_JOIN_ROWS; ++r) {
-    const int R = u.rt * N + r, tk = R >> a.gqa_shift;
-    if (tk >= u.n) return;
-    // a part without visible tokens (l = 0) has no reference
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int j = 0; j < parts; ++j) {
-      const float* p = (j ? rest + j * step : first) + N * D;
-      m = fmaxf(m, p[r] != 0.f ? p[N + r] : -INFINITY);
-    }
-    float o = 0.f, l = 0.f;
-#pragma unroll 4
-    for (int j = 0; j < parts; ++j) {
-      const float* p = j ? rest + j * step : first;
-      const float pl = p[N * D + r], f = pl != 0.f ? exp2f(p[N * D + N + r] - m) : 0.f;
-      o = fmaf(p[r * D + threadIdx.x], f, o);
-      l = fmaf(pl, f, l);
-    }
-    a.out[((size_t)(u.c0 + tk) * a.n_q_heads + u.h * a.gqa + (R & ((1 << a.gqa_shift) - 1))) * D + threadIdx.x] =
-        l != 0.f ? o / l : 0.f;
+  pdl_wait();
+  // the largest reference, of parts with visible tokens (l != 0)
+  float m = -INFINITY;
+  for (int j = lane; j < parts; j += 32) {
+    const float* p = (j ? rest + j * step : first) + N * D;
+    m = fmaxf(m, p[r] != 0.f ? p[N + r] : -INFINITY);
   }
+  m = warp_max(m);
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 8
+  for (int j = 0; j < parts; ++j) {
+    const float* p = j ? rest + j * step : first;
+    const float pl = p[N * D + r], f = pl != 0.f ? exp2f(p[N * D + N + r] - m) : 0.f;
+    const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * lane);
+    o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
+    l = fmaf(pl, f, l);
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  *reinterpret_cast<float4*>(a.out + ((size_t)(u.c0 + tk) * a.n_q_heads + u.h * a.gqa + (R & (a.gqa - 1))) * D + 4 * lane) =
+      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
 template <typename K, typename... A>
@@ -1199,11 +1281,19 @@ static cudaError_t qb_launch(const QbArgs& a, const int32_t* parents, const void
   cudaError_t e = smem_limit_once(attr, qb_attend_kernel<N>, qb_smem_bytes(N));
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.n_total * a.n_q_heads;
-  const long long blocks = 1 + (a.mode == QB_TREE ? a.n_seqs : 0) + (rows + QB_PREP_THREADS / 32 - 1) / (QB_PREP_THREADS / 32);
-  qb_prepare_kernel<N><<<(unsigned)blocks, QB_PREP_THREADS, 0, s>>>(a, parents, q, dtype, rot);
+  long long blocks = (rows + QB_PREP_THREADS / 32 - 1) / (QB_PREP_THREADS / 32);
+  int chunks = 1;
+  if (rot.kind == KVQ_ROT_DENSE) {  // about four blocks an SM, each with R's limbs split once
+    const int per_chunk = a.g.n_kv_heads * (D / QB_ROT_COLS);
+    const long long tiles = ((long long)a.n_total * a.gqa + QB_ROT_ROWS - 1) / QB_ROT_ROWS, most = 4 * grid / per_chunk;
+    chunks = (int)std::max<long long>(1, std::min(tiles, most));
+    blocks = (long long)per_chunk * chunks;
+  }
+  blocks += 1 + (a.mode == QB_TREE ? a.n_seqs : 0);
+  qb_prepare_kernel<N><<<(unsigned)blocks, QB_PREP_THREADS, 0, s>>>(a, parents, q, dtype, rot, chunks);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = qb_launch_pdl(qb_attend_kernel<N>, dim3(grid), QB_THREADS, qb_smem_bytes(N), s, a)) != cudaSuccess) return e;
-  return qb_launch_pdl(qb_combine_kernel<N>, dim3(grid, N / QB_JOIN_ROWS), D, 0, s, a, grid);
+  return qb_launch_pdl(qb_combine_kernel<N>, dim3(grid, N / QB_JOIN_ROWS), 32 * QB_JOIN_ROWS, 0, s, a, grid);
 }
 
 cudaError_t launch_query_block(const PageGeom& g, int n_q_heads, int n_seqs, int n_total, const void* q, int dtype,
