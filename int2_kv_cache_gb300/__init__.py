@@ -330,24 +330,38 @@ def kvq_decode_attention_win(layout: KvqLayout, q, seq_lens, max_seq_len: int, b
 
 
 # ---- speculative decoding and cross attention over the cache ----
-def _dense(t, name: str, dtype, shape):
-    """A dense tensor of this type and shape (None in the shape: any size) on the current CUDA device."""
+def _device_and_stream(stream):
+    """The current CUDA device (-2 without one: every tensor is then refused) and the raw stream of a call on it."""
     import torch
-    if t.dtype != dtype:
+    try:
+        dev = torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2, None
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, getattr(stream, "cuda_stream", stream)
+
+
+def _dense(t, name: str, dtype, shape, dev: int):
+    """The address of a dense tensor of this type and shape (None: any) on the current device."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return _ptr(_contig(t, name))
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _pool(layout: KvqLayout, pool):
+def _pool(layout: KvqLayout, pool, dev: int):
     """The cache pool: uint8 of any shape, no smaller than the layout's."""
     import torch
-    if pool.numel() < kvq_pool_bytes(layout):
-        raise ValueError(f"pool has {pool.numel()} bytes, the layout needs {kvq_pool_bytes(layout)}")
-    return _dense(pool, "pool", torch.uint8, tuple(pool.shape))
+    need = layout.num_blocks * layout.n_kv_heads * layout.page_tokens * 72
+    if pool.numel() < need:
+        raise ValueError(f"pool has {pool.numel()} bytes, the layout needs {need}")
+    return _dense(pool, "pool", torch.uint8, None, dev)
 
 
 def kvq_plan_workspace_size(n_seqs: int) -> int:
@@ -362,14 +376,17 @@ def kvq_plan_pages(layout: KvqLayout, old_lens, new_lens, block_table, free_ring
     free pages in place (counters (head, tail): ring_in -> ring_out, int64 [2]); cu_new int32 [n + 1] and slot_map
     int64 [capacity for new tokens] are written.  See include/kvq.h."""
     import torch
-    n, i32, i64 = old_lens.shape[0], torch.int32, torch.int64
+    i32, i64 = torch.int32, torch.int64
+    dev, raw = _device_and_stream(stream)
+    n, room = old_lens.shape[0], slot_map.shape[0]
     _check(lib().kvq_plan_pages(
-        ctypes.byref(layout), n, _dense(old_lens, "old_lens", i32, (n,)), _dense(new_lens, "new_lens", i32, (n,)),
-        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq)),
-        _dense(free_ring, "free_ring", i32, (layout.num_blocks,)), _dense(ring_in, "ring_in", i64, (2,)),
-        _dense(ring_out, "ring_out", i64, (2,)), slot_map.shape[0], _dense(cu_new, "cu_new", i32, (n + 1,)),
-        _dense(slot_map, "slot_map", i64, (None,)), _dense(workspace, "workspace", torch.uint8, (None,)),
-        workspace.numel(), _stream(stream)))
+        ctypes.byref(layout), n, _dense(old_lens, "old_lens", i32, (n,), dev),
+        _dense(new_lens, "new_lens", i32, (n,), dev),
+        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq), dev),
+        _dense(free_ring, "free_ring", i32, (layout.num_blocks,), dev), _dense(ring_in, "ring_in", i64, (2,), dev),
+        _dense(ring_out, "ring_out", i64, (2,), dev), room, _dense(cu_new, "cu_new", i32, (n + 1,), dev),
+        _dense(slot_map, "slot_map", i64, (room,), dev), _dense(workspace, "workspace", torch.uint8, None, dev),
+        workspace.numel(), raw))
 
 
 def kvq_query_block_workspace_size(layout: KvqLayout, n_seqs: int, n_q_total: int, max_q: int, max_seq_len: int) -> int:
@@ -385,28 +402,34 @@ def kvq_tree_attention(layout: KvqLayout, q, cu_q, max_q: int, parents, seq_lens
     over their own ancestors; the drafts are the last of the seq_lens[b] cached tokens.  parents: int32 [n_q_total]
     (index within the sequence, -1: follows the cache), or None for a chain (a causal chunk).  o_rot: fp32 like q."""
     import torch
-    n, total, i32 = seq_lens.shape[0], q.shape[0], torch.int32
+    i32 = torch.int32
+    dev, raw = _device_and_stream(stream)
+    n, total = seq_lens.shape[0], q.shape[0]
+    rows = (total, layout.n_q_heads, HEAD_DIM)
     _check(lib().kvq_tree_attention(
-        ctypes.byref(layout), n, total, _dense(q, "q", q.dtype, (total, layout.n_q_heads, HEAD_DIM)), _dtype_code(q),
-        _dense(cu_q, "cu_q", i32, (n + 1,)), max_q,
-        None if parents is None else _dense(parents, "parents", i32, (total,)),
-        _dense(seq_lens, "seq_lens", i32, (n,)), max_seq_len,
-        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq)), rot_k.c, _pool(layout, pool),
-        _dense(workspace, "workspace", torch.uint8, (None,)), workspace.numel(),
-        _dense(o_rot, "o_rot", torch.float32, (total, layout.n_q_heads, HEAD_DIM)), _stream(stream)))
+        ctypes.byref(layout), n, total, _dense(q, "q", q.dtype, rows, dev), _dtype_code(q),
+        _dense(cu_q, "cu_q", i32, (n + 1,), dev), max_q,
+        None if parents is None else _dense(parents, "parents", i32, (total,), dev),
+        _dense(seq_lens, "seq_lens", i32, (n,), dev), max_seq_len,
+        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq), dev), rot_k.c,
+        _pool(layout, pool, dev), _dense(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
+        _dense(o_rot, "o_rot", torch.float32, rows, dev), raw))
 
 
 def kvq_cross_attention(layout: KvqLayout, q, cu_q, max_q: int, state_lens, max_state_len: int, block_table,
                         rot_k: DeviceRot, pool, workspace, o_rot, stream=None) -> None:
     """Attention of query blocks over all cached states of their sequence (an encoder's), without a mask."""
     import torch
-    n, total, i32 = state_lens.shape[0], q.shape[0], torch.int32
+    i32 = torch.int32
+    dev, raw = _device_and_stream(stream)
+    n, total = state_lens.shape[0], q.shape[0]
+    rows = (total, layout.n_q_heads, HEAD_DIM)
     _check(lib().kvq_cross_attention(
-        ctypes.byref(layout), n, total, _dense(q, "q", q.dtype, (total, layout.n_q_heads, HEAD_DIM)), _dtype_code(q),
-        _dense(cu_q, "cu_q", i32, (n + 1,)), max_q, _dense(state_lens, "state_lens", i32, (n,)), max_state_len,
-        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq)), rot_k.c, _pool(layout, pool),
-        _dense(workspace, "workspace", torch.uint8, (None,)), workspace.numel(),
-        _dense(o_rot, "o_rot", torch.float32, (total, layout.n_q_heads, HEAD_DIM)), _stream(stream)))
+        ctypes.byref(layout), n, total, _dense(q, "q", q.dtype, rows, dev), _dtype_code(q),
+        _dense(cu_q, "cu_q", i32, (n + 1,), dev), max_q, _dense(state_lens, "state_lens", i32, (n,), dev),
+        max_state_len, _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq), dev), rot_k.c,
+        _pool(layout, pool, dev), _dense(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
+        _dense(o_rot, "o_rot", torch.float32, rows, dev), raw))
 
 
 def kvq_tree_commit(layout: KvqLayout, cu_q, accepted, n_accepted, slot_map, seq_lens, new_lens, pool,
@@ -414,12 +437,15 @@ def kvq_tree_commit(layout: KvqLayout, cu_q, accepted, n_accepted, slot_map, seq
     """Moves the accepted drafts' records (accepted int32 [n, max_accept], increasing; n_accepted int32 [n]) to the
     places of the first drafts and writes new_lens = seq_lens - drafts + accepted."""
     import torch
-    n, i32 = seq_lens.shape[0], torch.int32
+    i32 = torch.int32
+    dev, raw = _device_and_stream(stream)
+    n, total = seq_lens.shape[0], slot_map.shape[0]
+    depth = accepted.shape[1]
     _check(lib().kvq_tree_commit(
-        ctypes.byref(layout), n, slot_map.shape[0], accepted.shape[1], _dense(cu_q, "cu_q", i32, (n + 1,)),
-        _dense(accepted, "accepted", i32, (n, None)), _dense(n_accepted, "n_accepted", i32, (n,)),
-        _dense(slot_map, "slot_map", torch.int64, (None,)), _dense(seq_lens, "seq_lens", i32, (n,)),
-        _dense(new_lens, "new_lens", i32, (n,)), _pool(layout, pool), _stream(stream)))
+        ctypes.byref(layout), n, total, depth, _dense(cu_q, "cu_q", i32, (n + 1,), dev),
+        _dense(accepted, "accepted", i32, (n, depth), dev), _dense(n_accepted, "n_accepted", i32, (n,), dev),
+        _dense(slot_map, "slot_map", torch.int64, (total,), dev), _dense(seq_lens, "seq_lens", i32, (n,), dev),
+        _dense(new_lens, "new_lens", i32, (n,), dev), _pool(layout, pool, dev), raw))
 
 
 def kvq_fold_wo(w_o, n_q_heads: int, n_kv_heads: int, rot_v: DeviceRot, w_folded, stream=None) -> None:

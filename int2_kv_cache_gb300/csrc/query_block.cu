@@ -43,6 +43,7 @@
 // qb_combine_kernel joins in slice order (results do not depend on timing).
 #include <algorithm>
 #include <cstddef>
+#include <type_traits>
 
 #include "quant_common.cuh"
 #include "tcgen05.cuh"
@@ -356,10 +357,15 @@ __device__ __forceinline__ void qb_rotate_dense(const QbArgs& a, int h, int slic
                                                 uint2 (*s_b)[8][QB_ROT_COLS / 8][32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // R's limbs as B fragments: [limb][16-channel step][8 columns][lane = 4 (column % 8) + pair]
-  for (int p = warp; p < 64; p += QB_PREP_THREADS / 32) {  // channels 2p, 2p + 1; a lane a column
-    const float* r = dense + ((size_t)h * D + 2 * p) * D + QB_ROT_COLS * slice + lane;
+  const float* r_in = dense + (size_t)h * D * D + QB_ROT_COLS * slice + lane;
+  float2 v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = make_float2(__ldg(r_in + (2 * (warp + 8 * j)) * D), __ldg(r_in + (2 * (warp + 8 * j) + 1) * D));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int p = warp + 8 * j;  // channels 2p, 2p + 1; a lane a column
     uint32_t limb[3];
-    qb_split3(__ldg(r), __ldg(r + D), limb);
+    qb_split3(v[j].x, v[j].y, limb);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
       reinterpret_cast<uint32_t*>(&s_b[i][p >> 3][lane >> 3][4 * (lane & 7) + (p & 3)])[(p >> 2) & 1] = limb[i];
@@ -371,20 +377,25 @@ __device__ __forceinline__ void qb_rotate_dense(const QbArgs& a, int h, int slic
   for (long long r0 = (long long)chunk * QB_ROT_ROWS; r0 < rows; r0 += (long long)chunks * QB_ROT_ROWS) {
     const int ra = (int)r0 + 16 * rg + g, rb = ra + 8;
     const size_t oa = offset(min(ra, rows - 1)), ob = offset(min(rb, rows - 1));
+    using In = std::conditional_t<F32, float2, uint32_t>;  // two channels
+    In in[8][4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // rows g, g + 8; channels 2t, 2t + 1 and 8 further
+        in[k][i] = __ldg(static_cast<const In*>(q) + (((i & 1) ? ob : oa) + 16 * k + 2 * t + 8 * (i >> 1)) / 2);
     float d[2][4] = {};
-#pragma unroll 2
+#pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t x[F32 ? 3 : 1][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // rows g, g + 8; channels 2t, 2t + 1 and 8 further
-        const size_t at = ((i & 1) ? ob : oa) + 16 * k + 2 * t + 8 * (i >> 1);
+      for (int i = 0; i < 4; ++i) {
         if constexpr (F32) {
-          const float2 v = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(q) + at));
           uint32_t limb[3];
-          qb_split3(v.x, v.y, limb);
+          qb_split3(in[k][i].x, in[k][i].y, limb);
           x[0][i] = limb[0]; x[1][i] = limb[1]; x[2][i] = limb[2];
         } else {
-          x[0][i] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(q) + at));
+          x[0][i] = in[k][i];
         }
       }
 #pragma unroll
