@@ -43,7 +43,6 @@
 // qb_combine_kernel joins in slice order (results do not depend on timing).
 #include <algorithm>
 #include <cstddef>
-#include <type_traits>
 
 #include "quant_common.cuh"
 #include "tcgen05.cuh"
@@ -329,11 +328,16 @@ __device__ __forceinline__ void qb_rotate_row(const QbArgs& a, long long r, cons
 }
 
 // Dense rotations: a block takes 32 columns of one KV head's R and every `chunks`-th tile of
-// 64 of its rows.  fp32 values are split into three bf16 limbs (24 bits, exact), bf16 queries
+// its rows.  fp32 values are split into three bf16 limbs (24 bits, exact), bf16 queries
 // are one; the products whose limbs count from 2^0 to 2^-16 are taken on mma.sync (m16n8k16,
 // fp32 accumulation), 3 for bf16 queries and 6 for fp32, smallest first: about 2^-22 relative.
-// The rotation is a few per cent of the attention's work, so it needs no tensor memory.
-constexpr int QB_ROT_ROWS = 64, QB_ROT_COLS = 32;
+// The order of the channels in the products is free: step s gives thread t of a row the
+// channels 8 (4 (s / 2) + t) + 4 (s % 2) + 0 .. 3, so that it loads its part of a row as four
+// runs of 8 channels.  The rotation is a few per cent of the attention's work, so it needs no
+// tensor memory; with a load per channel pair instead it was bound by the load pipe (8 x 447 x
+// 16 rows: 49 us).
+constexpr int QB_ROT_COLS = 32;
+__host__ __device__ constexpr int qb_rot_rows(bool f32) { return f32 ? 64 : 128; }
 
 __device__ __forceinline__ void qb_split3(float x, float y, uint32_t (&limb)[3]) {
 #pragma unroll
@@ -368,61 +372,80 @@ __device__ __forceinline__ void qb_rotate_dense(const QbArgs& a, int h, int slic
     qb_split3(v[j].x, v[j].y, limb);
 #pragma unroll
     for (int i = 0; i < 3; ++i)
-      reinterpret_cast<uint32_t*>(&s_b[i][p >> 3][lane >> 3][4 * (lane & 7) + (p & 3)])[(p >> 2) & 1] = limb[i];
+      reinterpret_cast<uint32_t*>(&s_b[i][2 * (p >> 4) + ((p >> 1) & 1)][lane >> 3][4 * (lane & 7) + ((p >> 2) & 3)])[p & 1] = limb[i];
   }
   __syncthreads();
   const int rows = a.n_total << a.gqa_shift, gm = a.gqa - 1;  // n_total * n_q_heads < 2^31
+  constexpr int MT = qb_rot_rows(F32) / 64, RUN = F32 ? 2 : 1;  // 16-row tiles a warp; 16-byte loads a run
   const int rg = warp & 3, cg = warp >> 2, g = lane >> 2, t = lane & 3;
   auto offset = [&](int r) { return ((size_t)(r >> a.gqa_shift) * a.n_q_heads + h * a.gqa + (r & gm)) * D; };
-  for (long long r0 = (long long)chunk * QB_ROT_ROWS; r0 < rows; r0 += (long long)chunks * QB_ROT_ROWS) {
-    const int ra = (int)r0 + 16 * rg + g, rb = ra + 8;
-    const size_t oa = offset(min(ra, rows - 1)), ob = offset(min(rb, rows - 1));
-    using In = std::conditional_t<F32, float2, uint32_t>;  // two channels
-    In in[8][4];
+  for (long long r0 = (long long)chunk * 64 * MT; r0 < rows; r0 += (long long)chunks * 64 * MT) {
+    size_t o[MT][2];  // rows g and g + 8 of the warp's tiles
+    uint4 in[MT][2][4][RUN];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)  // rows g, g + 8; channels 2t, 2t + 1 and 8 further
-        in[k][i] = __ldg(static_cast<const In*>(q) + (((i & 1) ? ob : oa) + 16 * k + 2 * t + 8 * (i >> 1)) / 2);
-    float d[2][4] = {};
+      for (int i = 0; i < 2; ++i) {
+        o[m][i] = offset(min((int)r0 + 16 * MT * rg + 16 * m + 8 * i + g, rows - 1));
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < RUN; ++e)
+            in[m][i][c][e] = __ldg(static_cast<const uint4*>(q) + (o[m][i] + 32 * c + 8 * t) / (F32 ? 4 : 8) + e);
+      }
+    float d[MT][2][4] = {};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      uint32_t x[F32 ? 3 : 1][4];
+      uint32_t x[MT][F32 ? 3 : 1][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (F32) {
-          uint32_t limb[3];
-          qb_split3(in[k][i].x, in[k][i].y, limb);
-          x[0][i] = limb[0]; x[1][i] = limb[1]; x[2][i] = limb[2];
-        } else {
-          x[0][i] = in[k][i];
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (F32) {
+            const uint4 w = in[m][i][k >> 1][k & 1];
+            uint32_t lo[3], hi[3];
+            qb_split3(__uint_as_float(w.x), __uint_as_float(w.y), lo);
+            qb_split3(__uint_as_float(w.z), __uint_as_float(w.w), hi);
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+              x[m][e][i] = lo[e];
+              x[m][e][2 + i] = hi[e];
+            }
+          } else {
+            const uint4 w = in[m][i][k >> 1][0];
+            x[m][0][i] = k & 1 ? w.z : w.x;
+            x[m][0][2 + i] = k & 1 ? w.w : w.y;
+          }
         }
-      }
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         uint2 b[3];
 #pragma unroll
         for (int i = 0; i < 3; ++i) b[i] = s_b[i][k][2 * cg + n][lane];
-        if constexpr (F32) {
-          qb_mma_bf16(d[n], x[2], b[0]);
-          qb_mma_bf16(d[n], x[1], b[1]);
-          qb_mma_bf16(d[n], x[0], b[2]);
-          qb_mma_bf16(d[n], x[1], b[0]);
-        } else {
-          qb_mma_bf16(d[n], x[0], b[2]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (F32) {
+            qb_mma_bf16(d[m][n], x[m][2], b[0]);
+            qb_mma_bf16(d[m][n], x[m][1], b[1]);
+            qb_mma_bf16(d[m][n], x[m][0], b[2]);
+            qb_mma_bf16(d[m][n], x[m][1], b[0]);
+          } else {
+            qb_mma_bf16(d[m][n], x[m][0], b[2]);
+          }
+          qb_mma_bf16(d[m][n], x[m][0], b[1]);
+          qb_mma_bf16(d[m][n], x[m][0], b[0]);
         }
-        qb_mma_bf16(d[n], x[0], b[1]);
-        qb_mma_bf16(d[n], x[0], b[0]);
       }
     }
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int col = QB_ROT_COLS * slice + 16 * cg + 8 * n + 2 * t;
-      if (ra < rows)
-        *reinterpret_cast<float2*>(a.ws.q + oa + col) = make_float2(d[n][0] * QB_SCALE, d[n][1] * QB_SCALE);
-      if (rb < rows)
-        *reinterpret_cast<float2*>(a.ws.q + ob + col) = make_float2(d[n][2] * QB_SCALE, d[n][3] * QB_SCALE);
-    }
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if ((int)r0 + 16 * MT * rg + 16 * m + 8 * i + g < rows)
+            *reinterpret_cast<float2*>(a.ws.q + o[m][i] + QB_ROT_COLS * slice + 16 * cg + 8 * n + 2 * t) =
+                make_float2(d[m][n][2 * i] * QB_SCALE, d[m][n][2 * i + 1] * QB_SCALE);
   }
 }
 
@@ -1296,7 +1319,8 @@ static cudaError_t qb_launch(const QbArgs& a, const int32_t* parents, const void
   int chunks = 1;
   if (rot.kind == KVQ_ROT_DENSE) {  // about four blocks an SM, each with R's limbs split once
     const int per_chunk = a.g.n_kv_heads * (D / QB_ROT_COLS);
-    const long long tiles = ((long long)a.n_total * a.gqa + QB_ROT_ROWS - 1) / QB_ROT_ROWS, most = 4 * grid / per_chunk;
+    const int tile = qb_rot_rows(dtype == KVQ_F32);
+    const long long tiles = ((long long)a.n_total * a.gqa + tile - 1) / tile, most = 4 * grid / per_chunk;
     chunks = (int)std::max<long long>(1, std::min(tiles, most));
     blocks = (long long)per_chunk * chunks;
   }
