@@ -568,12 +568,12 @@ __device__ __forceinline__ float qb_max3(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ int qb_ordered(float f) {
-  const int i = __float_as_int(f);
-  return i ^ ((i >> 31) & 0x7fffffff);
+// Maximum over the warp (of what is not NaN).
+__device__ __forceinline__ float qb_warp_max(float x) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
 }
-__device__ __forceinline__ float qb_unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
-
 __device__ __forceinline__ float qb_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -607,15 +607,14 @@ template <int N>
 struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) float sumq[2][N];     // per row of the unit's queries: sum(q')
   alignas(16) int tin[2][N];
-  alignas(16) float neg_m[N];       // -M of the running unit
+  alignas(16) float neg_m[2][N];    // -M, 0 at first
   alignas(16) float scale[4][N];    // factors of the accumulated numerator for tile i (i % 4), where flagged
   alignas(8) int moved[4][2];       // per half of the rows: whether tile i (i % 4) moved a reference
-  alignas(16) int red[2][4][32];    // per half: the rows' maxima per warp
-  int fresh[2];                     // per half: whether a row has seen nothing yet
+  alignas(16) float red[2][4][32];  // per half: the rows' maxima per warp
+  alignas(8) float delta[2][32];    // per half: how far the references moved
   alignas(16) float tok[4][5][QB_TOK];  // constants of tile i (i % 4): see QB_C_*
   alignas(16) float lsum[4][N];
   alignas(16) float zsum[4][N];
-  alignas(16) float m_out[N];
   alignas(16) QbUnit unit[QB_UNITS];
   float unscale[2];                 // what the products of key codes and queries are scaled back by
   float qmax[2][4];
@@ -626,7 +625,7 @@ struct QbShared {  // alignas: read as 16-byte vectors
   uint64_t q_ready[2];
   uint64_t k_ready[2], v_ready[2], s_done[2], s_free[2], p_ready[2], o_done[2], o_free[2];
   uint64_t lz_ready, lz_free, last;
-  uint64_t group[3];                // meetings of the four warps of a softmax half (0, 1) and of the accumulation (2)
+  uint64_t group;                   // meetings of the four accumulation warps
   uint32_t tmem;
 };
 static_assert(offsetof(QbShared<16>, neg_m) % 16 == 0 && offsetof(QbShared<16>, tok) % 16 == 0 &&
@@ -671,7 +670,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
     mbar_init(&sh.lz_ready, 8);
     mbar_init(&sh.lz_free, 4);
     mbar_init(&sh.last, 1);
-    for (int i = 0; i < 3; ++i) mbar_init(&sh.group[i], 4);
+    mbar_init(&sh.group, 4);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -695,21 +694,21 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
     int left = WAIT_LIMIT;
 #pragma unroll 1
     while (!__all_sync(FULLM, mbar_try_wait(bar, parity & 1)))
-      if (--left == 0) {
-        if (lane == 0) flag_error(a.err, ERR_TIMEOUT);
-        return false;
-      }
+      if (--left == 0) return false;
     return true;
+  };
+  auto gave_up = [&]() {
+    if (lane == 0) flag_error(a.err, ERR_TIMEOUT);
   };
   auto arrive = [&](uint64_t* bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  // the four warps of a group meet (a bounded wait, unlike a hardware barrier)
+  // the four accumulation warps meet (a bounded wait, unlike a hardware barrier)
   uint32_t round = 0;
-  auto meet = [&](int group) {
-    arrive(&sh.group[group]);
-    return wait(&sh.group[group], round++);
+  auto meet = [&]() {
+    arrive(&sh.group);
+    return wait(&sh.group, round++);
   };
 
   if (n_tiles > 0) {
@@ -726,7 +725,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       const int v_off = (vt >> ps) * a.g.record + (32 << ps) + 32 * (vt & pm) + 16 * vh;
       // this warp's value fields 2 warp and 2 warp + 1 are bits 4 warp .. 4 warp + 3: rotated to bits 4 .. 7
       const int v_rotate = (4 * warp - 4) & 31;
-      for (int i = 0; i < n_tiles; ++i) {
+      int i = 0;
+      for (; i < n_tiles; ++i) {
         const int st = i % QB_STAGES, buf = i & 1, use = i >> 1;
         const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
         if (!wait(&sh.full[st], i / QB_STAGES)) break;
@@ -792,6 +792,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         tc_fence_before();
         arrive(&sh.v_ready[buf]);
       }
+      if (i < n_tiles) gave_up();
     } else if (warp < 12) {
       // ---- softmax: one token a thread, rows col0 .. col0 + NH - 1 ----
       if constexpr (N == 64) qb_registers<136, true>();
@@ -802,6 +803,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       float unscale = 0.f;
       const float* s_sumq = nullptr;
       const int* s_tin = nullptr;
+      float* s_neg_m = nullptr;
       int un = -1, t = 0, t1 = 0, base = 0, open = 0, len = 0, c0 = 0;
       bool unset = false, fresh = false;
       uint64_t l2[NH / 2], z2[NH / 2];
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         const int buf = i & 1, use = i >> 1;
         if (t == t1 && ok) {
           ++un;
-          if ((ok = wait(&sh.unit_full[un % QB_UNITS], un / QB_UNITS) && wait(&sh.q_ready[un & 1], un >> 1) && meet(half))) {
+          if ((ok = wait(&sh.unit_full[un % QB_UNITS], un / QB_UNITS) && wait(&sh.q_ready[un & 1], un >> 1))) {
             const QbUnit& u = sh.unit[un % QB_UNITS];
             t = u.t0;
             t1 = u.t1;
@@ -825,10 +827,9 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             unscale = sh.unscale[un & 1];
             s_sumq = sh.sumq[un & 1];
             s_tin = sh.tin[un & 1];
-            if (tok < NH) sh.neg_m[col0 + tok] = 0.f;
+            s_neg_m = sh.neg_m[un & 1];
             unset = tok < NH;  // row col0 + tok has seen nothing yet, and M = 0
             fresh = true;      // some row has not
-            ok = meet(half);
 #pragma unroll
             for (int j = 0; j < NH / 2; ++j) l2[j] = z2[j] = 0ull;
           }
@@ -849,7 +850,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
           if (!ok || !wait(&sh.s_done[buf], use)) {
             ok = false;
-            qb_vote(1 + half, false);
+            if (qb_vote(1 + half, false)) {  // the others move their references
+              qb_vote(1 + half, false);
+              qb_vote(1 + half, false);
+            }
             continue;
           }
           tc_fence_after();
@@ -860,84 +864,64 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
                          zc2 = f2pk(zc, zc);
           uint8_t* p_hi = s_p + (2 * buf) * QB_PBUF + tok * 128;
           const uint32_t scores = tmem + lanes + T_S + 64 * buf + col0;
-          // the references move up to the rows' maxima over the 128 tokens (rare: a short loop, off the common path)
-          auto move_references = [&]() {
-            int row_max = 0;
-#pragma unroll 1
-            for (int j = 0; j < NH; j += 8) {
-              float v[8];
-              tmem_ld8(scores + j, v);
+          if (lead) sh.moved[i & 3][half] = 0;
+          // x: a + log2 s - M, -infinity where the row does not see the token
+          float x[NH], top = -INFINITY;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int col = col0 + j + k;
-                v[k] = fmaf(sk, v[k], fmaf(kz, s_sumq[col], sh.neg_m[col] + ls));
-                if ((unsigned)(s_tin[col] - key_tin) >= key_size) v[k] = -INFINITY;
-                const int m = __reduce_max_sync(FULLM, qb_ordered(v[k]));
-                if (lane == j + k) row_max = m;
-              }
+          for (int c = 0; c < NC; ++c) qb_tmem_ld<CH>(scores + c * CH, *reinterpret_cast<float(*)[CH]>(x + c * CH));
+#pragma unroll
+          for (int j = 0; j < NH; j += 4) {
+            const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col0 + j);
+            const float4 nm = *reinterpret_cast<const float4*>(s_neg_m + col0 + j);
+            const uint64_t u0 = f2fma(kz2, f2pk(sq.x, sq.y), f2add(f2pk(nm.x, nm.y), ls2));
+            const uint64_t u1 = f2fma(kz2, f2pk(sq.z, sq.w), f2add(f2pk(nm.z, nm.w), ls2));
+            const float2 d0 = f2up(f2fma(sk2, f2pk(x[j], x[j + 1]), u0));
+            const float2 d1 = f2up(f2fma(sk2, f2pk(x[j + 2], x[j + 3]), u1));
+            x[j] = d0.x; x[j + 1] = d0.y; x[j + 2] = d1.x; x[j + 3] = d1.y;
+          }
+          if (__builtin_expect(masked, 0)) {
+#pragma unroll
+            for (int j = 0; j < NH; ++j) x[j] = (unsigned)(s_tin[col0 + j] - key_tin) < key_size ? x[j] : -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < NH; j += 2) top = qb_max3(top, x[j], x[j + 1]);
+          // whether any weight of the 128 tokens would pass the limit
+          if (__builtin_expect(qb_vote(1 + half, top > QB_TRIGGER || fresh), 0)) {
+            // the references move up to the rows' maxima over the 128 tokens
+            float row_max = 0.f;
+#pragma unroll
+            for (int j = 0; j < NH; ++j) {
+              const float m = qb_warp_max(x[j]);
+              if (lane == j) row_max = m;
             }
             if (lane < NH) sh.red[half][q4][lane] = row_max;
-            if (!meet(half)) return false;
-            if (q4 == 0) {
-              if (tok < NH) {
-                const float m = qb_unordered(max(max(sh.red[half][0][tok], sh.red[half][1][tok]),
-                                                 max(sh.red[half][2][tok], sh.red[half][3][tok])));
-                const float by = (unset ? m > -INFINITY : m > 0.f) ? m : 0.f;
-                sh.neg_m[col0 + tok] -= by;
-                sh.scale[i & 3][col0 + tok] = unset ? 1.f : qb_ex2(-by);  // nothing to scale yet
-                if (m > -INFINITY) unset = false;
-              }
-              const bool some = __any_sync(FULLM, unset);
-              if (lane == 0) {
-                sh.fresh[half] = some;
-                sh.moved[i & 3][half] = 1;
-              }
+            qb_vote(1 + half, false);
+            bool some = false;
+            if (tok < NH) {
+              const float m = fmaxf(fmaxf(sh.red[half][0][tok], sh.red[half][1][tok]),
+                                    fmaxf(sh.red[half][2][tok], sh.red[half][3][tok]));
+              const float by = (unset ? m > -INFINITY : m > 0.f) ? m : 0.f;
+              s_neg_m[col0 + tok] -= by;
+              sh.delta[half][tok] = by;
+              sh.scale[i & 3][col0 + tok] = unset ? 1.f : qb_ex2(-by);  // nothing to scale yet
+              if (m > -INFINITY) unset = false;
+              some = unset;
+              if (lead) sh.moved[i & 3][half] = 1;
             }
-            if (!meet(half)) return false;
-            fresh = sh.fresh[half] != 0;
+            fresh = qb_vote(1 + half, some);
 #pragma unroll
             for (int j = 0; j < NH; j += 2) {
               const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col0 + j);
+              const float2 by = *reinterpret_cast<const float2*>(sh.delta[half] + j);
               const uint64_t f2 = f2pk(f.x, f.y);
               l2[j / 2] = f2mul(l2[j / 2], f2);
               z2[j / 2] = f2mul(z2[j / 2], f2);
+              x[j] -= by.x;
+              x[j + 1] -= by.y;
             }
-            return true;
-          };
-          if (lead) sh.moved[i & 3][half] = 0;
-          float x[NH], top;
-          auto logits = [&]() {  // x: a + log2 s - M, -infinity where the row does not see the token; top: the largest
-#pragma unroll
-            for (int c = 0; c < NC; ++c) qb_tmem_ld<CH>(scores + c * CH, *reinterpret_cast<float(*)[CH]>(x + c * CH));
-#pragma unroll
-            for (int j = 0; j < NH; j += 4) {
-              const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col0 + j);
-              const float4 nm = *reinterpret_cast<const float4*>(sh.neg_m + col0 + j);
-              const uint64_t u0 = f2fma(kz2, f2pk(sq.x, sq.y), f2add(f2pk(nm.x, nm.y), ls2));
-              const uint64_t u1 = f2fma(kz2, f2pk(sq.z, sq.w), f2add(f2pk(nm.z, nm.w), ls2));
-              const float2 d0 = f2up(f2fma(sk2, f2pk(x[j], x[j + 1]), u0));
-              const float2 d1 = f2up(f2fma(sk2, f2pk(x[j + 2], x[j + 3]), u1));
-              x[j] = d0.x; x[j + 1] = d0.y; x[j + 2] = d1.x; x[j + 3] = d1.y;
-            }
-            if (__builtin_expect(masked, 0)) {
-#pragma unroll
-              for (int j = 0; j < NH; ++j) x[j] = (unsigned)(s_tin[col0 + j] - key_tin) < key_size ? x[j] : -INFINITY;
-            }
-            top = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < NH; j += 2) top = qb_max3(top, x[j], x[j + 1]);
-          };
-          logits();
-          // whether any weight of the 128 tokens would pass the limit
-          const bool move = qb_vote(1 + half, top > QB_TRIGGER || fresh);
+          }
 #pragma unroll
           for (int j = 0; j < NH; ++j) x[j] = qb_ex2(x[j]);
-          if (__builtin_expect(move, 0)) {
-            if (!(ok = move_references())) continue;
-            logits();
-#pragma unroll
-            for (int j = 0; j < NH; ++j) x[j] = qb_ex2(x[j]);
-          }
           tc_fence_before();  // the scores are in registers
           arrive(&sh.s_free[buf]);
           if (use && !(ok = wait(&sh.o_done[buf], use - 1))) continue;
@@ -966,8 +950,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
         }
         if (t + 1 < t1) continue;
-        // the unit's l and sum p mid over the 128 tokens: every thread leaves its NH values where its weights of the
-        // next tile will go, and adds one row up over 32 tokens
+        // the unit's l and sum p mid over the warp's 32 tokens: every thread leaves its NH values where its weights of
+        // the next tile will go, and adds one row up
         if ((i > 0 && !(ok = wait(&sh.o_done[(i - 1) & 1], (i - 1) >> 1))) || (un && !(ok = wait(&sh.lz_free, un - 1))))
           continue;
         uint8_t* mine = s_p + 2 * ((i + 1) & 1) * QB_PBUF;
@@ -981,19 +965,18 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             const float2 p = f2up(pass ? z2[j / 2] : l2[j / 2]), q = f2up(pass ? z2[j / 2 + 1] : l2[j / 2 + 1]);
             *reinterpret_cast<float4*>(at(j, tok)) = make_float4(p.x, p.y, q.x, q.y);
           }
-          if (!(ok = meet(half))) break;
+          __syncwarp();
           if (lane < NH) {
             float sum = 0.f;
-#pragma unroll 2
+#pragma unroll 4
             for (int k = 0; k < 32; ++k) sum += reinterpret_cast<const float*>(at(lane, 32 * q4 + k))[lane & 3];
             (pass ? sh.zsum : sh.lsum)[q4][col0 + lane] = sum;
           }
-          if (!(ok = meet(half))) break;
+          __syncwarp();
         }
-        if (!ok) continue;
-        if (tok < NH) sh.m_out[col0 + tok] = -sh.neg_m[col0 + tok];
         arrive(&sh.lz_ready);
       }
+      if (!ok) gave_up();
     } else if (warp < 16) {
       // ---- accumulation: one channel a thread ----
       const int q4 = warp & 3, wt = tid - 384;
@@ -1004,6 +987,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       const int from = 16 * (wt & 7) + (wt >> 3);
       QbUnit u{};
       int i = 0;
+      bool done = false;
       // round un: the queries of unit un + 1 into their buffer, then unit un
       for (int un = -1;; ++un) {
         if (!wait(&sh.unit_full[(un + 1) % QB_UNITS], (un + 1) / QB_UNITS)) break;
@@ -1028,7 +1012,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
 #pragma unroll
           for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(FULLM, m, d));
           if (lane == 0) sh.qmax[buf][q4] = m;
-          if (!meet(2)) break;
+          if (!meet()) break;
           m = fmaxf(fmaxf(sh.qmax[buf][0], sh.qmax[buf][1]), fmaxf(sh.qmax[buf][2], sh.qmax[buf][3]));
           // the largest at 2^8 .. 2^9, times up to 2^6 for the keys' fields
           const int e = m > 0.f ? min(100, max(-100, 8 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
@@ -1062,6 +1046,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
           if (part == 0) {
             sh.sumq[buf][row] = s;
+            sh.neg_m[buf][row] = 0.f;
             sh.tin[buf][row] =
                 !valid ? 0 : a.mode == QB_TREE ? a.ws.tree[next.c0 + tk].x : a.mode == QB_CHAIN ? tk : 0;
           }
@@ -1109,11 +1094,11 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             sh.row_f[wt] = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
             if (!whole) {
               part_out[N * D + wt] = l;
-              part_out[N * D + N + wt] = sh.m_out[wt];
+              part_out[N * D + N + wt] = -sh.neg_m[un & 1][wt];
             }
           }
           arrive(&sh.lz_free);
-          if (!meet(2)) break;
+          if (!meet()) break;
           const int rows = min(N, (u.n << gs) - u.rt * N);
           float* out = a.out + ((size_t)u.c0 * a.n_q_heads + u.h * a.gqa) * D + wt;
 #pragma unroll 4
@@ -1123,11 +1108,15 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             if (whole) out[((size_t)(R >> gs) * a.n_q_heads + (R & gm)) * D] = o;
             else part_out[j * D + wt] = o;
           }
-          if (!meet(2)) break;  // the staging rows may be written again
+          if (!meet()) break;  // the staging rows may be written again
         }
-        if (next.t1 == next.t0) break;
+        if (next.t1 == next.t0) {
+          done = true;
+          break;
+        }
         u = next;
       }
+      if (!done) gave_up();
     } else if (warp == 16) {
       if constexpr (N == 64) qb_registers<40, false>();
       // ---- page copies, and the list of units one ahead of them ----
@@ -1174,8 +1163,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         }
         u = ahead;
       }
-      if (!ok)  // no copy in flight when the CTA ends
+      if (!ok) {  // no copy in flight when the CTA ends
+        gave_up();
         for (int k = max(0, i - QB_STAGES); k < i; ++k) mbar_wait_bounded(&sh.full[k % QB_STAGES], (k / QB_STAGES) & 1);
+      }
     } else if (warp > 17) {
       if constexpr (N == 64) qb_registers<40, false>();
     } else {
@@ -1228,6 +1219,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         }
       }
       if (!ok) {  // let the tensor cores finish before their memory is freed
+        gave_up();
         if (qb_elect()) tc_commit(&sh.last);
         __syncwarp();
         mbar_wait_bounded(&sh.last, 0);
