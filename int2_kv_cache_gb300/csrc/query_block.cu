@@ -967,10 +967,12 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
           __syncwarp();
           if (lane < NH) {
-            float sum = 0.f;
-#pragma unroll 4
-            for (int k = 0; k < 32; ++k) sum += reinterpret_cast<const float*>(at(lane, 32 * q4 + k))[lane & 3];
-            (pass ? sh.zsum : sh.lsum)[q4][col0 + lane] = sum;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+            for (int k = 0; k < 32; k += 4)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum[e] += reinterpret_cast<const float*>(at(lane, 32 * q4 + k + e))[lane & 3];
+            (pass ? sh.zsum : sh.lsum)[q4][col0 + lane] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
           __syncwarp();
         }
@@ -983,8 +985,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       constexpr int TPR = 128 / N;  // threads a query row
       const int row = wt / TPR, part = wt % TPR, gs = a.gqa_shift, gm = (1 << gs) - 1;
-      // channel `wt` is held by the thread of tensor-memory lane 16 f + g (f = channel % 8, g = channel / 8)
-      const int from = 16 * (wt & 7) + (wt >> 3);
+      // channel 8 g + f is in tensor-memory lane 16 f + g: this thread's channels 4 lane .. 4 lane + 3 are 16 lanes apart
+      const int from = 64 * (lane & 1) + (lane >> 1);
       QbUnit u{};
       int i = 0;
       bool done = false;
@@ -998,14 +1000,19 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           const bool valid = tk < next.n;
           const float* src =
               a.ws.q + ((size_t)(next.c0 + (valid ? tk : 0)) * a.n_q_heads + next.h * a.gqa + (R & gm)) * D + part * N;
-          float m = 0.f, s = 0.f;
-#pragma unroll 2
-          for (int j = 0; j < N; j += 4) {
-            const float4 v = valid ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-            s += (v.x + v.y) + (v.z + v.w);
-            const float w[4] = {fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w)};
+          // all of a thread's loads at once: with a round trip per load this took 8 us a unit
+          float v[N];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m = w[k] <= 3.0e38f ? fmaxf(m, w[k]) : m;  // of the finite ones
+          for (int j = 0; j < N; j += 4) {
+            const float4 x = valid ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[j] = x.x; v[j + 1] = x.y; v[j + 2] = x.z; v[j + 3] = x.w;
+          }
+          float m = 0.f, s = 0.f;
+#pragma unroll
+          for (int j = 0; j < N; ++j) {
+            s += v[j];
+            const float w = fabsf(v[j]);
+            m = w <= 3.0e38f ? fmaxf(m, w) : m;  // of the finite ones
           }
 #pragma unroll
           for (int d = 1; d < TPR; d <<= 1) s += __shfl_xor_sync(FULLM, s, d);
@@ -1018,23 +1025,17 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           const int e = m > 0.f ? min(100, max(-100, 8 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
           const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
           uint8_t* dst = s_q + buf * N * 512 + row * 128;
-#pragma unroll 1
-          for (int j = 0; j < N; j += 16) {
-            float v[16];
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 x = valid ? *reinterpret_cast<const float4*>(src + j + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-              v[k] = x.x * scale; v[k + 1] = x.y * scale; v[k + 2] = x.z * scale; v[k + 3] = x.w * scale;
-            }
+          for (int j = 0; j < N; j += 16) {
             // K order of the expanded keys: channels f and 8 + f of a 16-channel word side by side
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int f = 0; f < 8; ++f) {
-              v[f] *= (float)(1 << (8 - qb_bit(f)));
-              v[8 + f] *= (float)(1 << (8 - qb_bit(f)));
-              hi[f] = qb_half2(v[f], v[8 + f]);
+              const float up = scale * (float)(1 << (8 - qb_bit(f)));
+              const float x = v[j + f] * up, y = v[j + 8 + f] * up;
+              hi[f] = qb_half2(x, y);
               const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[f]));
-              lo[f] = qb_half2(v[f] - back.x, v[8 + f] - back.y);
+              lo[f] = qb_half2(x - back.x, y - back.y);
             }
             const int w = (part * N + j) >> 4;  // 16-channel word
             uint8_t* d = dst + (w >> 2) * N * 128;
@@ -1100,13 +1101,14 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           arrive(&sh.lz_free);
           if (!meet()) break;
           const int rows = min(N, (u.n << gs) - u.rt * N);
-          float* out = a.out + ((size_t)u.c0 * a.n_q_heads + u.h * a.gqa) * D + wt;
-#pragma unroll 4
-          for (int j = 0; j < rows; ++j) {
-            const float o = (s_out[j * D + from] + sh.row_z[j]) * sh.row_f[j];
+          float* out = a.out + ((size_t)u.c0 * a.n_q_heads + u.h * a.gqa) * D + 4 * lane;
+#pragma unroll 2
+          for (int j = q4; j < rows; j += 4) {
+            const float *o = s_out + j * D + from, z = sh.row_z[j], f = sh.row_f[j];
+            const float4 y = make_float4((o[0] + z) * f, (o[16] + z) * f, (o[32] + z) * f, (o[48] + z) * f);
             const int R = u.rt * N + j;
-            if (whole) out[((size_t)(R >> gs) * a.n_q_heads + (R & gm)) * D] = o;
-            else part_out[j * D + wt] = o;
+            float* to = whole ? out + ((size_t)(R >> gs) * a.n_q_heads + (R & gm)) * D : part_out + j * D + 4 * lane;
+            *reinterpret_cast<float4*>(to) = y;
           }
           if (!meet()) break;  // the staging rows may be written again
         }
