@@ -30,14 +30,14 @@
 // reference, the maximum of the first tile, moved only when a weight would pass
 // 2^14: one vote a tile, and most units never move it again.
 //
-// A CTA (18 warps, one per SM, persistent over an equal slice of all tiles):
+// A CTA (one per SM, persistent over an equal slice of all tiles):
 //   warps 0-3    expand the codes of a tile into tensor memory: a thread owns a token
 //                (keys) or, through a transposing load, 16 channels of a field (values)
-//   warps 4-11   softmax: a thread owns a token, each half of the warps half of the
+//   2 or 4 groups of four softmax warps: a thread owns a token, a group 8 or 16 of the
 //                rows; weights go to shared memory as the next product's B operand
-//   warps 12-15  add up the 128-token products, load the next unit's queries, write out
-//   warp 16      page copies (cp.async.bulk) and the list of units
-//   warp 17      issues the MMAs
+//   4 warps      add up the 128-token products, load the next unit's queries, write out
+//   1 warp       page copies (cp.async.bulk) and the list of units
+//   1 warp       issues the MMAs
 // A unit is (sequence, KV head, row tile).  Slices cut units: a unit wholly inside a
 // CTA is written out at once, a cut one leaves partials (numerator, l, M) that
 // qb_combine_kernel joins in slice order (results do not depend on timing).
@@ -54,10 +54,14 @@ constexpr float QB_SCALE = 0.12751742902274214f;  // log2(e) / sqrt(128): base-2
 constexpr int QB_TOK = 128;                       // tokens a tile
 constexpr int QB_STAGES = 4;
 constexpr int QB_STAGE_BYTES = QB_TOK * 72;
-constexpr int QB_THREADS = 20 * 32;                // 18 warps work; register shares go by groups of four warps
 constexpr int QB_PBUF = QB_TOK * 128;             // one half of W^T: 128 rows of 128 bytes (64 fp16 columns)
 constexpr int QB_UNITS = 4;                       // ring of unit descriptors
 constexpr float QB_TRIGGER = 14.f;                // the reference moves to the running maximum when a weight would pass 2^14
+
+// Groups of four softmax warps: 16 rows each (8 for the 16-row tile).
+__host__ __device__ constexpr int qb_groups(int n) { return n == 64 ? 4 : 2; }
+// Expansion (4 warps), softmax, accumulation (4), copies, MMA issue and two idle warps: register shares go by four warps.
+__host__ __device__ constexpr int qb_threads(int n) { return 32 * (12 + 4 * qb_groups(n)); }
 
 __host__ __device__ constexpr int qb_smem_bytes(int n) {
   return 1024 + 2 * n * 512 + 2 * 2 * QB_PBUF + QB_STAGES * QB_STAGE_BYTES + n * D * 4;
@@ -609,9 +613,9 @@ struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) int tin[2][N];
   alignas(16) float neg_m[2][N];    // -M, 0 at first
   alignas(16) float scale[4][N];    // factors of the accumulated numerator for tile i (i % 4), where flagged
-  alignas(8) int moved[4][2];       // per half of the rows: whether tile i (i % 4) moved a reference
-  alignas(16) float red[2][4][32];  // per half: the rows' maxima per warp
-  alignas(8) float delta[2][32];    // per half: how far the references moved
+  alignas(16) int moved[4][qb_groups(N)];            // per group: whether tile i (i % 4) moved a reference
+  alignas(16) float red[qb_groups(N)][4][16];        // per group: the rows' maxima per warp
+  alignas(8) float delta[qb_groups(N)][16];          // per group: how far the references moved
   alignas(16) float tok[4][5][QB_TOK];  // constants of tile i (i % 4): see QB_C_*
   alignas(16) float lsum[4][N];
   alignas(16) float zsum[4][N];
@@ -623,7 +627,11 @@ struct QbShared {  // alignas: read as 16-byte vectors
   uint64_t empty[QB_STAGES];
   uint64_t unit_full[QB_UNITS], unit_free[QB_UNITS];
   uint64_t q_ready[2];
-  uint64_t k_ready[2], v_ready[2], s_done[2], s_free[2], p_ready[2], o_done[2], o_free[2];
+  // by tile parity.  k_ready: its keys are expanded.  p_ready: its weights and values are there and the products of
+  // two tiles earlier are read (softmax, expansion and accumulation warps arrive).  s_done, o_done: the tensor cores have
+  // finished its scores, its readout.  They work in order - scores of i + 1, readout of i - so s_done(i) also says
+  // that the readout of i - 2 is finished with its weights, and p_ready(i - 2) that the scores of i - 2 are read.
+  uint64_t k_ready[2], p_ready[2], s_done[2], o_done[2];
   uint64_t lz_ready, lz_free, last;
   uint64_t group;                   // meetings of the four accumulation warps
   uint32_t tmem;
@@ -633,10 +641,10 @@ static_assert(offsetof(QbShared<16>, neg_m) % 16 == 0 && offsetof(QbShared<16>, 
               "vector reads");
 
 template <int N>
-__global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
-  constexpr int NH = N / 2;                     // rows of a softmax half
-  constexpr int CH = NH < 16 ? NH : 16;         // rows of a chunk
-  constexpr int NC = NH / CH;                   // chunks of a half
+__global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
+  constexpr int NG = qb_groups(N), NH = N / NG;  // groups of softmax warps, rows of a group
+  constexpr int W_ACC = 4 + 4 * NG, W_COPY = W_ACC + 4, W_MMA = W_COPY + 1;  // first warps of the roles
+  static_assert(NH == 8 || NH == 16, "rows of a softmax group");
   constexpr uint32_t T_K = 0, T_V = 128, T_S = 256, T_O = 384;  // tensor memory columns, two buffers of 64 each
   extern __shared__ uint8_t qb_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(qb_raw) + 1023) & ~uintptr_t(1023));
@@ -655,19 +663,16 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
     }
     for (int i = 0; i < QB_UNITS; ++i) {
       mbar_init(&sh.unit_full[i], 1);
-      mbar_init(&sh.unit_free[i], 8 + 4 + 1);
+      mbar_init(&sh.unit_free[i], 4 * NG + 4 + 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_ready[i], 4);
       mbar_init(&sh.k_ready[i], 4);
-      mbar_init(&sh.v_ready[i], 4);
       mbar_init(&sh.s_done[i], 1);
-      mbar_init(&sh.s_free[i], 8);
-      mbar_init(&sh.p_ready[i], 8);
+      mbar_init(&sh.p_ready[i], 4 + 4 * NG + 4);
       mbar_init(&sh.o_done[i], 1);
-      mbar_init(&sh.o_free[i], 4);
     }
-    mbar_init(&sh.lz_ready, 8);
+    mbar_init(&sh.lz_ready, 4 * NG);
     mbar_init(&sh.lz_free, 4);
     mbar_init(&sh.last, 1);
     mbar_init(&sh.group, 4);
@@ -714,7 +719,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
   if (n_tiles > 0) {
     if (warp < 4) {
       // ---- codes -> tensor memory, and the tokens' constants ----
-      if constexpr (N == 64) qb_registers<72, false>();
+      if constexpr (N == 64) qb_registers<48, false>();
       const uint32_t lanes = (uint32_t)(32 * warp) << 16;
       const int ps = a.page_shift, pm = (1 << ps) - 1;
       const int tok = 32 * warp + lane;
@@ -725,52 +730,58 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       const int v_off = (vt >> ps) * a.g.record + (32 << ps) + 32 * (vt & pm) + 16 * vh;
       // this warp's value fields 2 warp and 2 warp + 1 are bits 4 warp .. 4 warp + 3: rotated to bits 4 .. 7
       const int v_rotate = (4 * warp - 4) & 31;
-      int i = 0;
-      for (; i < n_tiles; ++i) {
-        const int st = i % QB_STAGES, buf = i & 1, use = i >> 1;
-        const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
-        if (!wait(&sh.full[st], i / QB_STAGES)) break;
-        {
-          const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off));
-          const float2 vm = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off + (4 << ps)));
-          const float sv = vm.x == 0.f ? 5.9604644775390625e-08f : vm.x;
-          float ls = __log2f(sv), inv = __fdividef(1.f, sv), zc = inv * fmaf(1.5f, sv, vm.y);
-          if (!(fabsf(zc) <= 3.4e38f)) {  // not finite: NaN for the rows that see the token, 0 * 0 for the others
-            ls = NAN;
-            inv = zc = 0.f;
+      int i = -1;
+      for (; i < n_tiles; ++i) {  // the keys of tile i + 1, then the values of tile i
+        const int j = i + 1;
+        if (j < n_tiles) {
+          const int st = j % QB_STAGES, buf = j & 1;
+          const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
+          if (!wait(&sh.full[st], j / QB_STAGES)) break;
+          {
+            const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off));
+            const float2 vm = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off + (4 << ps)));
+            const float sv = vm.x == 0.f ? 5.9604644775390625e-08f : vm.x;
+            float ls = __log2f(sv), inv = __fdividef(1.f, sv), zc = inv * fmaf(1.5f, sv, vm.y);
+            if (!(fabsf(zc) <= 3.4e38f)) {  // not finite: NaN for the rows that see the token, 0 * 0 for the others
+              ls = NAN;
+              inv = zc = 0.f;
+            }
+            float(*c)[QB_TOK] = sh.tok[j & 3];
+            c[QB_C_SK][tok] = km.x;
+            c[QB_C_KZ][tok] = km.y;
+            c[QB_C_LS][tok] = ls;
+            c[QB_C_INV][tok] = inv;
+            c[QB_C_ZC][tok] = zc;
           }
-          float(*c)[QB_TOK] = sh.tok[i & 3];
-          c[QB_C_SK][tok] = km.x;
-          c[QB_C_KZ][tok] = km.y;
-          c[QB_C_LS][tok] = ls;
-          c[QB_C_INV][tok] = inv;
-          c[QB_C_ZC][tok] = zc;
-        }
-        if (use && !wait(&sh.s_done[buf], use - 1)) break;
-        tc_fence_after();
-        // short loops on purpose: straight-line code runs at the speed of the instruction fetch
+          if (j >= 2 && !wait(&sh.s_done[buf], (j >> 1) - 1)) break;
+          tc_fence_after();
+          // short loops on purpose: straight-line code runs at the speed of the instruction fetch
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const uint2 w = *reinterpret_cast<const uint2*>(stage + k_off + 8 * k);
-          uint32_t r[16];
+          for (int k = 0; k < 4; ++k) {
+            const uint2 w = *reinterpret_cast<const uint2*>(stage + k_off + 8 * k);
+            uint32_t r[16];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t x = j ? w.y : w.x, y = qb_swap(x);
-            r[8 * j + 0] = qb_key_field<0>(x, y);
-            r[8 * j + 1] = qb_key_field<1>(x, y);
-            r[8 * j + 2] = qb_key_field<2>(x, y);
-            r[8 * j + 3] = qb_key_field<3>(x, y);
-            r[8 * j + 4] = qb_key_field<4>(x, y);
-            r[8 * j + 5] = qb_key_field<5>(x, y);
-            r[8 * j + 6] = qb_key_field<6>(x, y);
-            r[8 * j + 7] = qb_key_field<7>(x, y);
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t x = e ? w.y : w.x, y = qb_swap(x);
+              r[8 * e + 0] = qb_key_field<0>(x, y);
+              r[8 * e + 1] = qb_key_field<1>(x, y);
+              r[8 * e + 2] = qb_key_field<2>(x, y);
+              r[8 * e + 3] = qb_key_field<3>(x, y);
+              r[8 * e + 4] = qb_key_field<4>(x, y);
+              r[8 * e + 5] = qb_key_field<5>(x, y);
+              r[8 * e + 6] = qb_key_field<6>(x, y);
+              r[8 * e + 7] = qb_key_field<7>(x, y);
+            }
+            tmem_st16(tmem + lanes + T_K + 64 * buf + 16 * k, r);
           }
-          tmem_st16(tmem + lanes + T_K + 64 * buf + 16 * k, r);
+          tmem_wait_st();
+          tc_fence_before();
+          arrive(&sh.k_ready[buf]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        arrive(&sh.k_ready[buf]);
-        if (use && !wait(&sh.o_done[buf], use - 1)) break;
+        if (i < 0) continue;
+        const int st = i % QB_STAGES, buf = i & 1;
+        const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
+        if (i >= 2 && !wait(&sh.o_done[buf], (i >> 1) - 1)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {  // 32 tokens: 16 columns
@@ -790,16 +801,16 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         arrive(&sh.empty[st]);
         tmem_wait_st();
         tc_fence_before();
-        arrive(&sh.v_ready[buf]);
+        arrive(&sh.p_ready[buf]);
       }
       if (i < n_tiles) gave_up();
-    } else if (warp < 12) {
+    } else if (warp < W_ACC) {
       // ---- softmax: one token a thread, rows col0 .. col0 + NH - 1 ----
-      if constexpr (N == 64) qb_registers<136, true>();
-      const int half = (warp - 4) >> 2, q4 = warp & 3, col0 = half * NH;
+      if constexpr (N == 64) qb_registers<80, true>();
+      const int group = (warp - 4) >> 2, q4 = warp & 3, col0 = group * NH;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       const int tok = 32 * q4 + lane;
-      const bool lead = tid == 128 + 128 * half;
+      const bool lead = tid == 128 + 128 * group;
       float unscale = 0.f;
       const float* s_sumq = nullptr;
       const int* s_tin = nullptr;
@@ -850,9 +861,9 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
           if (!ok || !wait(&sh.s_done[buf], use)) {
             ok = false;
-            if (qb_vote(1 + half, false)) {  // the others move their references
-              qb_vote(1 + half, false);
-              qb_vote(1 + half, false);
+            if (qb_vote(1 + group, false)) {  // the others move their references
+              qb_vote(1 + group, false);
+              qb_vote(1 + group, false);
             }
             continue;
           }
@@ -864,11 +875,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
                          zc2 = f2pk(zc, zc);
           uint8_t* p_hi = s_p + (2 * buf) * QB_PBUF + tok * 128;
           const uint32_t scores = tmem + lanes + T_S + 64 * buf + col0;
-          if (lead) sh.moved[i & 3][half] = 0;
+          if (lead) sh.moved[i & 3][group] = 0;
           // x: a + log2 s - M, -infinity where the row does not see the token
           float x[NH], top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < NC; ++c) qb_tmem_ld<CH>(scores + c * CH, *reinterpret_cast<float(*)[CH]>(x + c * CH));
+          qb_tmem_ld<NH>(scores, x);
 #pragma unroll
           for (int j = 0; j < NH; j += 4) {
             const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col0 + j);
@@ -886,7 +896,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
 #pragma unroll
           for (int j = 0; j < NH; j += 2) top = qb_max3(top, x[j], x[j + 1]);
           // whether any weight of the 128 tokens would pass the limit
-          if (__builtin_expect(qb_vote(1 + half, top > QB_TRIGGER || fresh), 0)) {
+          if (__builtin_expect(qb_vote(1 + group, top > QB_TRIGGER || fresh), 0)) {
             // the references move up to the rows' maxima over the 128 tokens
             float row_max = 0.f;
 #pragma unroll
@@ -894,25 +904,25 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
               const float m = qb_warp_max(x[j]);
               if (lane == j) row_max = m;
             }
-            if (lane < NH) sh.red[half][q4][lane] = row_max;
-            qb_vote(1 + half, false);
+            if (lane < NH) sh.red[group][q4][lane] = row_max;
+            qb_vote(1 + group, false);
             bool some = false;
             if (tok < NH) {
-              const float m = fmaxf(fmaxf(sh.red[half][0][tok], sh.red[half][1][tok]),
-                                    fmaxf(sh.red[half][2][tok], sh.red[half][3][tok]));
+              const float m = fmaxf(fmaxf(sh.red[group][0][tok], sh.red[group][1][tok]),
+                                    fmaxf(sh.red[group][2][tok], sh.red[group][3][tok]));
               const float by = (unset ? m > -INFINITY : m > 0.f) ? m : 0.f;
               s_neg_m[col0 + tok] -= by;
-              sh.delta[half][tok] = by;
+              sh.delta[group][tok] = by;
               sh.scale[i & 3][col0 + tok] = unset ? 1.f : qb_ex2(-by);  // nothing to scale yet
               if (m > -INFINITY) unset = false;
               some = unset;
-              if (lead) sh.moved[i & 3][half] = 1;
+              if (lead) sh.moved[i & 3][group] = 1;
             }
-            fresh = qb_vote(1 + half, some);
+            fresh = qb_vote(1 + group, some);
 #pragma unroll
             for (int j = 0; j < NH; j += 2) {
               const float2 f = *reinterpret_cast<const float2*>(sh.scale[i & 3] + col0 + j);
-              const float2 by = *reinterpret_cast<const float2*>(sh.delta[half] + j);
+              const float2 by = *reinterpret_cast<const float2*>(sh.delta[group] + j);
               const uint64_t f2 = f2pk(f.x, f.y);
               l2[j / 2] = f2mul(l2[j / 2], f2);
               z2[j / 2] = f2mul(z2[j / 2], f2);
@@ -922,9 +932,6 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
 #pragma unroll
           for (int j = 0; j < NH; ++j) x[j] = qb_ex2(x[j]);
-          tc_fence_before();  // the scores are in registers
-          arrive(&sh.s_free[buf]);
-          if (use && !(ok = wait(&sh.o_done[buf], use - 1))) continue;
 #pragma unroll
           for (int j = 0; j < NH; j += 8) {  // two fp16 halves of every weight
             uint32_t hi[4], lo[4];
@@ -940,6 +947,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(p_hi + QB_PBUF + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
+          tc_fence_before();
           fence_proxy_async();
           arrive(&sh.p_ready[buf]);
 #pragma unroll
@@ -979,9 +987,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         arrive(&sh.lz_ready);
       }
       if (!ok) gave_up();
-    } else if (warp < 16) {
+    } else if (warp < W_COPY) {
       // ---- accumulation: one channel a thread ----
-      const int q4 = warp & 3, wt = tid - 384;
+      if constexpr (N == 64) qb_registers<96, true>();
+      const int q4 = warp & 3, wt = tid - 32 * W_ACC;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       constexpr int TPR = 128 / N;  // threads a query row
       const int row = wt / TPR, part = wt % TPR, gs = a.gqa_shift, gm = (1 << gs) - 1;
@@ -990,6 +999,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       QbUnit u{};
       int i = 0;
       bool done = false;
+      arrive(&sh.p_ready[0]);  // nothing to read before tiles 0 and 1
+      arrive(&sh.p_ready[1]);
       // round un: the queries of unit un + 1 into their buffer, then unit un
       for (int un = -1;; ++un) {
         if (!wait(&sh.unit_full[(un + 1) % QB_UNITS], (un + 1) / QB_UNITS)) break;
@@ -1065,22 +1076,22 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             if (!(ok = wait(&sh.o_done[buf], use))) break;
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < N / CH; ++c) {
-              float o[CH];
-              qb_tmem_ld<CH>(tmem + lanes + T_O + 64 * buf + c * CH, o);
-              if (sh.moved[i & 3][c / NC]) {
+            for (int c = 0; c < NG; ++c) {
+              float o[NH];
+              qb_tmem_ld<NH>(tmem + lanes + T_O + 64 * buf + c * NH, o);
+              if (sh.moved[i & 3][c]) {
 #pragma unroll
-                for (int j = 0; j < CH; ++j) acc[c * CH + j] *= sh.scale[i & 3][c * CH + j];
+                for (int j = 0; j < NH; ++j) acc[c * NH + j] *= sh.scale[i & 3][c * NH + j];
               }
 #pragma unroll
-              for (int j = 0; j < CH; j += 2) {
-                const float2 s = f2up(f2add(f2pk(acc[c * CH + j], acc[c * CH + j + 1]), f2pk(o[j], o[j + 1])));
-                acc[c * CH + j] = s.x;
-                acc[c * CH + j + 1] = s.y;
+              for (int j = 0; j < NH; j += 2) {
+                const float2 s = f2up(f2add(f2pk(acc[c * NH + j], acc[c * NH + j + 1]), f2pk(o[j], o[j + 1])));
+                acc[c * NH + j] = s.x;
+                acc[c * NH + j + 1] = s.y;
               }
             }
             tc_fence_before();
-            arrive(&sh.o_free[buf]);
+            arrive(&sh.p_ready[buf]);  // for tile i + 2
           }
           if (!ok) break;
 #pragma unroll
@@ -1119,7 +1130,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         u = next;
       }
       if (!done) gave_up();
-    } else if (warp == 16) {
+    } else if (warp == W_COPY) {
       if constexpr (N == 64) qb_registers<40, false>();
       // ---- page copies, and the list of units one ahead of them ----
       QbUnit u = qb_locate<N>(a, first, lane), ahead;
@@ -1169,7 +1180,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         gave_up();
         for (int k = max(0, i - QB_STAGES); k < i; ++k) mbar_wait_bounded(&sh.full[k % QB_STAGES], (k / QB_STAGES) & 1);
       }
-    } else if (warp > 17) {
+    } else if (warp > W_MMA) {
       if constexpr (N == 64) qb_registers<40, false>();
     } else {
       if constexpr (N == 64) qb_registers<40, false>();
@@ -1189,7 +1200,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             q = sw128_desc(s_q + (un & 1) * N * 512);
           }
           --left;
-          if (!(ok = wait(&sh.k_ready[buf], use) && (!use || wait(&sh.s_free[buf], use - 1)))) break;
+          if (!(ok = wait(&sh.k_ready[buf], use))) break;
           tc_fence_after();
           if (qb_elect()) {
             const uint32_t ak = tmem + T_K + 64 * buf, d = tmem + T_S + 64 * buf;
@@ -1204,9 +1215,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         }
         if (i > 0) {
           const int buf = (i - 1) & 1, use = (i - 1) >> 1;
-          if (!(ok = wait(&sh.v_ready[buf], use) && wait(&sh.p_ready[buf], use) &&
-                     (!use || wait(&sh.o_free[buf], use - 1))))
-            break;
+          if (!(ok = wait(&sh.p_ready[buf], use))) break;
           tc_fence_after();
           if (qb_elect()) {
             const uint64_t hi = sw128_desc(s_p + (2 * buf) * QB_PBUF), lo = sw128_desc(s_p + (2 * buf + 1) * QB_PBUF);
@@ -1321,7 +1330,7 @@ static cudaError_t qb_launch(const QbArgs& a, const int32_t* parents, const void
   blocks += 1 + (a.mode == QB_TREE ? a.n_seqs : 0);
   qb_prepare_kernel<N><<<(unsigned)blocks, QB_PREP_THREADS, 0, s>>>(a, parents, q, dtype, rot, chunks);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = qb_launch_pdl(qb_attend_kernel<N>, dim3(grid), QB_THREADS, qb_smem_bytes(N), s, a)) != cudaSuccess) return e;
+  if ((e = qb_launch_pdl(qb_attend_kernel<N>, dim3(grid), qb_threads(N), qb_smem_bytes(N), s, a)) != cudaSuccess) return e;
   return qb_launch_pdl(qb_combine_kernel<N>, dim3(grid, N / QB_JOIN_ROWS), 32 * QB_JOIN_ROWS, 0, s, a, grid);
 }
 
