@@ -31,7 +31,7 @@
 // 2^14: one vote a tile, and most units never move it again.
 //
 // A CTA (one per SM, persistent over an equal slice of all tiles):
-//   warps 0-3    expand the codes of a tile into tensor memory: a thread owns a token
+//   4 + 4 warps  expand the codes of a tile into tensor memory: a thread owns a token
 //                (keys) or, through a transposing load, 16 channels of a field (values)
 //   2 or 4 groups of four softmax warps: a thread owns a token, a group 8 or 16 of the
 //                rows; weights go to shared memory as the next product's B operand
@@ -60,8 +60,8 @@ constexpr float QB_TRIGGER = 14.f;                // the reference moves to the 
 
 // Groups of four softmax warps: 16 rows each (8 for the 16-row tile).
 __host__ __device__ constexpr int qb_groups(int n) { return n == 64 ? 4 : 2; }
-// Expansion (4 warps), softmax, accumulation (4), copies, MMA issue and two idle warps: register shares go by four warps.
-__host__ __device__ constexpr int qb_threads(int n) { return 32 * (12 + 4 * qb_groups(n)); }
+// Keys (4 warps), values (4), softmax, accumulation (4), copies, MMA issue and two idle warps: register shares go by four.
+__host__ __device__ constexpr int qb_threads(int n) { return 32 * (16 + 4 * qb_groups(n)); }
 
 __host__ __device__ constexpr int qb_smem_bytes(int n) {
   return 1024 + 2 * n * 512 + 2 * 2 * QB_PBUF + QB_STAGES * QB_STAGE_BYTES + n * D * 4;
@@ -600,10 +600,21 @@ __device__ __forceinline__ bool qb_vote(int id, bool p) {
 }
 enum { QB_C_SK, QB_C_KZ, QB_C_LS, QB_C_INV, QB_C_ZC };
 
+// Register shares by role (a thread; 0: as launched): keys, values, softmax, accumulation, copies and MMA issue.  The
+// 64-row tile: 32 warps launched with 64 (sum 4 x 40 + 4 x 48 + 16 x 72 + 4 x 96 + 4 x 40 = 32 x 64); the 32-row tile: 24
+// with 80 (4 x 56 + 4 x 56 + 8 x 104 + 4 x 96 + 4 x 56 = 1888 <= 24 x 80).
+struct QbRegisters {
+  int keys, values, softmax, acc, misc;
+};
+__host__ __device__ constexpr QbRegisters qb_shares(int n) {
+  return n == 64 ? QbRegisters{40, 48, 72, 96, 40} : n == 32 ? QbRegisters{56, 56, 104, 96, 56} : QbRegisters{0, 0, 0, 0, 0};
+}
+
 // Register shares of a group of four warps (the block's total stays what it was launched with).
 template <int R, bool UP>
 __device__ __forceinline__ void qb_registers() {
-  if constexpr (UP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+  if constexpr (R == 0) return;
+  else if constexpr (UP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
@@ -643,7 +654,7 @@ static_assert(offsetof(QbShared<16>, neg_m) % 16 == 0 && offsetof(QbShared<16>, 
 template <int N>
 __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
   constexpr int NG = qb_groups(N), NH = N / NG;  // groups of softmax warps, rows of a group
-  constexpr int W_ACC = 4 + 4 * NG, W_COPY = W_ACC + 4, W_MMA = W_COPY + 1;  // first warps of the roles
+  constexpr int W_ACC = 8 + 4 * NG, W_COPY = W_ACC + 4, W_MMA = W_COPY + 1;  // first warps of the roles
   static_assert(NH == 8 || NH == 16, "rows of a softmax group");
   constexpr uint32_t T_K = 0, T_V = 128, T_S = 256, T_O = 384;  // tensor memory columns, two buffers of 64 each
   extern __shared__ uint8_t qb_raw[];
@@ -659,7 +670,7 @@ __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
   if (tid == 0) {
     for (int i = 0; i < QB_STAGES; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 4);
+      mbar_init(&sh.empty[i], 4 + 4);
     }
     for (int i = 0; i < QB_UNITS; ++i) {
       mbar_init(&sh.unit_full[i], 1);
@@ -718,69 +729,75 @@ __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
 
   if (n_tiles > 0) {
     if (warp < 4) {
-      // ---- codes -> tensor memory, and the tokens' constants ----
-      if constexpr (N == 64) qb_registers<48, false>();
+      // ---- key codes -> tensor memory, and the tokens' constants ----
+      qb_registers<qb_shares(N).keys, false>();
       const uint32_t lanes = (uint32_t)(32 * warp) << 16;
       const int ps = a.page_shift, pm = (1 << ps) - 1;
       const int tok = 32 * warp + lane;
       const int k_off = (tok >> ps) * a.g.record + 32 * (tok & pm);
       const int meta_off = (tok >> ps) * a.g.record + (64 << ps) + 4 * (tok & pm);
+      int i = 0;
+      for (; i < n_tiles; ++i) {
+        const int st = i % QB_STAGES, buf = i & 1;
+        const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
+        if (!wait(&sh.full[st], i / QB_STAGES)) break;
+        const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off));
+        const float2 vm = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off + (4 << ps)));
+        const float sv = vm.x == 0.f ? 5.9604644775390625e-08f : vm.x;
+        float ls = __log2f(sv), inv = __fdividef(1.f, sv), zc = inv * fmaf(1.5f, sv, vm.y);
+        if (!(fabsf(zc) <= 3.4e38f)) {  // not finite: NaN for the rows that see the token, 0 * 0 for the others
+          ls = NAN;
+          inv = zc = 0.f;
+        }
+        // the scores of tile i - 2 are done: its expanded keys may go, and the constants of tile i - 4 have been read
+        if (i >= 2 && !wait(&sh.s_done[buf], (i >> 1) - 1)) break;
+        float(*c)[QB_TOK] = sh.tok[i & 3];
+        c[QB_C_SK][tok] = km.x;
+        c[QB_C_KZ][tok] = km.y;
+        c[QB_C_LS][tok] = ls;
+        c[QB_C_INV][tok] = inv;
+        c[QB_C_ZC][tok] = zc;
+        tc_fence_after();
+        // short loops on purpose: straight-line code runs at the speed of the instruction fetch
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const uint2 w = *reinterpret_cast<const uint2*>(stage + k_off + 8 * k);
+          uint32_t r[16];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = e ? w.y : w.x, y = qb_swap(x);
+            r[8 * e + 0] = qb_key_field<0>(x, y);
+            r[8 * e + 1] = qb_key_field<1>(x, y);
+            r[8 * e + 2] = qb_key_field<2>(x, y);
+            r[8 * e + 3] = qb_key_field<3>(x, y);
+            r[8 * e + 4] = qb_key_field<4>(x, y);
+            r[8 * e + 5] = qb_key_field<5>(x, y);
+            r[8 * e + 6] = qb_key_field<6>(x, y);
+            r[8 * e + 7] = qb_key_field<7>(x, y);
+          }
+          tmem_st16(tmem + lanes + T_K + 64 * buf + 16 * k, r);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        arrive(&sh.k_ready[buf]);
+        arrive(&sh.empty[st]);
+      }
+      if (i < n_tiles) gave_up();
+    } else if (warp < 8) {
+      // ---- value codes -> tensor memory ----
+      qb_registers<qb_shares(N).values, false>();
+      const uint32_t lanes = (uint32_t)(32 * (warp - 4)) << 16;
+      const int ps = a.page_shift, pm = (1 << ps) - 1;
       // rows of the transposing loads: lane l gives row l % 8 of matrix l / 8; 16 tokens are 1152 bytes of either page size
       const int vt = (lane & 7) + ((lane >> 4) << 3), vh = (lane >> 3) & 1;
       const int v_off = (vt >> ps) * a.g.record + (32 << ps) + 32 * (vt & pm) + 16 * vh;
-      // this warp's value fields 2 warp and 2 warp + 1 are bits 4 warp .. 4 warp + 3: rotated to bits 4 .. 7
-      const int v_rotate = (4 * warp - 4) & 31;
-      int i = -1;
-      for (; i < n_tiles; ++i) {  // the keys of tile i + 1, then the values of tile i
-        const int j = i + 1;
-        if (j < n_tiles) {
-          const int st = j % QB_STAGES, buf = j & 1;
-          const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
-          if (!wait(&sh.full[st], j / QB_STAGES)) break;
-          {
-            const float2 km = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off));
-            const float2 vm = __half22float2(*reinterpret_cast<const __half2*>(stage + meta_off + (4 << ps)));
-            const float sv = vm.x == 0.f ? 5.9604644775390625e-08f : vm.x;
-            float ls = __log2f(sv), inv = __fdividef(1.f, sv), zc = inv * fmaf(1.5f, sv, vm.y);
-            if (!(fabsf(zc) <= 3.4e38f)) {  // not finite: NaN for the rows that see the token, 0 * 0 for the others
-              ls = NAN;
-              inv = zc = 0.f;
-            }
-            float(*c)[QB_TOK] = sh.tok[j & 3];
-            c[QB_C_SK][tok] = km.x;
-            c[QB_C_KZ][tok] = km.y;
-            c[QB_C_LS][tok] = ls;
-            c[QB_C_INV][tok] = inv;
-            c[QB_C_ZC][tok] = zc;
-          }
-          if (j >= 2 && !wait(&sh.s_done[buf], (j >> 1) - 1)) break;
-          tc_fence_after();
-          // short loops on purpose: straight-line code runs at the speed of the instruction fetch
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            const uint2 w = *reinterpret_cast<const uint2*>(stage + k_off + 8 * k);
-            uint32_t r[16];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x = e ? w.y : w.x, y = qb_swap(x);
-              r[8 * e + 0] = qb_key_field<0>(x, y);
-              r[8 * e + 1] = qb_key_field<1>(x, y);
-              r[8 * e + 2] = qb_key_field<2>(x, y);
-              r[8 * e + 3] = qb_key_field<3>(x, y);
-              r[8 * e + 4] = qb_key_field<4>(x, y);
-              r[8 * e + 5] = qb_key_field<5>(x, y);
-              r[8 * e + 6] = qb_key_field<6>(x, y);
-              r[8 * e + 7] = qb_key_field<7>(x, y);
-            }
-            tmem_st16(tmem + lanes + T_K + 64 * buf + 16 * k, r);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          arrive(&sh.k_ready[buf]);
-        }
-        if (i < 0) continue;
+      // a warp's fields 2 w and 2 w + 1 are bits 4 w .. 4 w + 3: rotated to bits 4 .. 7
+      const int v_rotate = (4 * (warp - 4) - 4) & 31;
+      int i = 0;
+      for (; i < n_tiles; ++i) {
         const int st = i % QB_STAGES, buf = i & 1;
         const uint8_t* stage = s_stage + st * QB_STAGE_BYTES;
+        if (!wait(&sh.full[st], i / QB_STAGES)) break;
         if (i >= 2 && !wait(&sh.o_done[buf], (i >> 1) - 1)) break;
         tc_fence_after();
 #pragma unroll 1
@@ -806,11 +823,11 @@ __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
       if (i < n_tiles) gave_up();
     } else if (warp < W_ACC) {
       // ---- softmax: one token a thread, rows col0 .. col0 + NH - 1 ----
-      if constexpr (N == 64) qb_registers<80, true>();
-      const int group = (warp - 4) >> 2, q4 = warp & 3, col0 = group * NH;
+      qb_registers<qb_shares(N).softmax, true>();
+      const int group = (warp - 8) >> 2, q4 = warp & 3, col0 = group * NH;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       const int tok = 32 * q4 + lane;
-      const bool lead = tid == 128 + 128 * group;
+      const bool lead = tid == 256 + 128 * group;
       float unscale = 0.f;
       const float* s_sumq = nullptr;
       const int* s_tin = nullptr;
@@ -989,7 +1006,7 @@ __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
       if (!ok) gave_up();
     } else if (warp < W_COPY) {
       // ---- accumulation: one channel a thread ----
-      if constexpr (N == 64) qb_registers<96, true>();
+      qb_registers<qb_shares(N).acc, true>();
       const int q4 = warp & 3, wt = tid - 32 * W_ACC;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       constexpr int TPR = 128 / N;  // threads a query row
@@ -1131,7 +1148,7 @@ __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
       }
       if (!done) gave_up();
     } else if (warp == W_COPY) {
-      if constexpr (N == 64) qb_registers<40, false>();
+      qb_registers<qb_shares(N).misc, false>();
       // ---- page copies, and the list of units one ahead of them ----
       QbUnit u = qb_locate<N>(a, first, lane), ahead;
       long long left = n_tiles;
@@ -1181,9 +1198,9 @@ __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
         for (int k = max(0, i - QB_STAGES); k < i; ++k) mbar_wait_bounded(&sh.full[k % QB_STAGES], (k / QB_STAGES) & 1);
       }
     } else if (warp > W_MMA) {
-      if constexpr (N == 64) qb_registers<40, false>();
+      qb_registers<qb_shares(N).misc, false>();
     } else {
-      if constexpr (N == 64) qb_registers<40, false>();
+      qb_registers<qb_shares(N).misc, false>();
       // ---- MMA issue ----
       constexpr uint32_t I_QK = qb_idesc(N, false), I_PV = qb_idesc(N, true);
       int un = -1, left = 0;
