@@ -33,7 +33,7 @@
 // A CTA (one per SM, persistent over an equal slice of all tiles):
 //   4 + 4 warps  expand the codes of a tile into tensor memory: a thread owns a token
 //                (keys) or, through a transposing load, 16 channels of a field (values)
-//   2 or 4 groups of four softmax warps: a thread owns a token, a group 8 or 16 of the
+//   2 x 4 warps  softmax: a thread owns a token, each group of four warps half of the
 //                rows; weights go to shared memory as the next product's B operand
 //   4 warps      add up the 128-token products, load the next unit's queries, write out
 //   1 warp       page copies (cp.async.bulk) and the list of units
@@ -56,12 +56,12 @@ constexpr int QB_STAGES = 4;
 constexpr int QB_STAGE_BYTES = QB_TOK * 72;
 constexpr int QB_PBUF = QB_TOK * 128;             // one half of W^T: 128 rows of 128 bytes (64 fp16 columns)
 constexpr int QB_UNITS = 4;                       // ring of unit descriptors
+constexpr int QB_UNIT_WORK = 3;                   // what starting and ending a unit costs, in tiles (measured: 5 us and 1.6 us)
 constexpr float QB_TRIGGER = 14.f;                // the reference moves to the running maximum when a weight would pass 2^14
 
-// Groups of four softmax warps: 16 rows each (8 for the 16-row tile).
-__host__ __device__ constexpr int qb_groups(int n) { return n == 64 ? 4 : 2; }
+constexpr int QB_GROUPS = 2;                      // groups of four softmax warps, half of the rows each
 // Keys (4 warps), values (4), softmax, accumulation (4), copies, MMA issue and two idle warps: register shares go by four.
-__host__ __device__ constexpr int qb_threads(int n) { return 32 * (16 + 4 * qb_groups(n)); }
+constexpr int QB_THREADS = 32 * (16 + 4 * QB_GROUPS);
 
 __host__ __device__ constexpr int qb_smem_bytes(int n) {
   return 1024 + 2 * n * 512 + 2 * 2 * QB_PBUF + QB_STAGES * QB_STAGE_BYTES + n * D * 4;
@@ -73,7 +73,8 @@ __host__ __device__ constexpr int qb_smem_bytes(int n) {
 struct QbWs {
   float* q;          // [n_total][n_q_heads][128] rotated, scaled queries
   int2* tree;        // [n_total] (tin, size)
-  long long* tiles;  // [n_seqs + 1] running sum of the sequences' tiles
+  long long* work;   // [n_seqs + 1] running sum of the sequences' work (tiles, and QB_UNIT_WORK a unit)
+  long long* tiles;  // [n_seqs + 1] running sum of their tiles
   float* part;       // [2 grid][N][130]: numerator [N][128], l [N], M [N]
 };
 
@@ -87,12 +88,14 @@ static int qb_rows(int max_q, int gqa) {
 
 static size_t qb_layout(void* base, int n_seqs, int n_total, int n_q_heads, int rows, int grid, QbWs* out) {
   const size_t o_tree = qb_align((size_t)n_total * n_q_heads * D * sizeof(float));
-  const size_t o_tiles = qb_align(o_tree + (size_t)n_total * sizeof(int2));
+  const size_t o_work = qb_align(o_tree + (size_t)n_total * sizeof(int2));
+  const size_t o_tiles = qb_align(o_work + ((size_t)n_seqs + 1) * sizeof(long long));
   const size_t o_part = qb_align(o_tiles + ((size_t)n_seqs + 1) * sizeof(long long));
   if (out) {
     char* p = static_cast<char*>(base);
     out->q = reinterpret_cast<float*>(p);
     out->tree = reinterpret_cast<int2*>(p + o_tree);
+    out->work = reinterpret_cast<long long*>(p + o_work);
     out->tiles = reinterpret_cast<long long*>(p + o_tiles);
     out->part = reinterpret_cast<float*>(p + o_part);
   }
@@ -168,7 +171,8 @@ __device__ __forceinline__ QbSpan qb_span(const QbArgs& a, const QbSeq& q) {
   return s;
 }
 
-// Slice k of all tiles: [start(k), start(k + 1)), sizes equal to within one.
+// Slice k of all work: [start(k), start(k + 1)), sizes equal to within one.  A unit's work is QB_UNIT_WORK, then one per
+// tile; a slice has the tiles whose work lies in it.
 struct QbSlices {
   long long each;
   int more;
@@ -183,13 +187,14 @@ struct QbUnit {
   int t0, t1, nt;     // tiles [t0, t1) of nt in this slice
 };
 
-// The unit that holds tile `t` of all, by one warp; u.t0 = the tile inside the unit.
+// The unit that holds the work at `w`, by one warp: u.t0 = the first of its tiles at or after w; `in`: w inside the unit;
+// `before`: the tiles of all that come before w.
 template <int N>
-__device__ __forceinline__ QbUnit qb_locate(const QbArgs& a, long long t, int lane) {
+__device__ __forceinline__ QbUnit qb_locate(const QbArgs& a, long long w, int lane, int& in, long long& before) {
   int lo = 0, cnt = a.n_seqs;
-  while (cnt > 1) {  // the last sequence that starts at or before t
+  while (cnt > 1) {  // the last sequence that starts at or before w
     const int step = (cnt + 31) / 32, i = lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, i < cnt && a.ws.tiles[lo + i] <= t);
+    const unsigned m = __ballot_sync(0xffffffffu, i < cnt && a.ws.work[lo + i] <= w);
     const int k = 31 - __clz(m);
     lo += k * step;
     cnt = min(step, cnt - k * step);
@@ -199,22 +204,25 @@ __device__ __forceinline__ QbUnit qb_locate(const QbArgs& a, long long t, int la
   const QbSeq q = qb_seq(a, lo, nullptr);
   const QbSpan s = qb_span<N>(a, q);
   const int H = a.g.n_kv_heads;
-  const long long rem = t - a.ws.tiles[lo];
+  const long long rem = w - a.ws.work[lo];
   int j0 = 0, j1 = s.n_rt;
   while (j1 - j0 > 1) {
     const int mid = (j0 + j1) >> 1;
-    if (s.before(mid) * H <= rem) j0 = mid;
+    if ((s.before(mid) + (long long)QB_UNIT_WORK * mid) * H <= rem) j0 = mid;
     else j1 = mid;
   }
   u.rt = j0;
   u.nt = s.tiles(j0);
-  const long long in = rem - s.before(j0) * H;
-  u.h = (int)(in / u.nt);
-  u.t0 = (int)(in % u.nt);
+  const long long rest = rem - (s.before(j0) + (long long)QB_UNIT_WORK * j0) * H;  // < (nt + QB_UNIT_WORK) H < 2^31
+  const unsigned each = (unsigned)(u.nt + QB_UNIT_WORK);
+  u.h = (int)((unsigned)rest / each);
+  in = (int)((unsigned)rest % each);
+  u.t0 = max(0, in - QB_UNIT_WORK);
   u.t1 = u.nt;
   u.c0 = q.c0;
   u.n = q.n;
   u.len = q.len;
+  before = a.ws.tiles[lo] + s.before(j0) * H + (long long)u.h * u.nt + u.t0;
   return u;
 }
 
@@ -251,27 +259,46 @@ constexpr int QB_PREP_THREADS = 256;
 
 template <int N>
 __device__ __forceinline__ void qb_list_tiles(const QbArgs& a) {
-  __shared__ long long s_warp[QB_PREP_THREADS / 32];
+  __shared__ long long s_warp[2][QB_PREP_THREADS / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (a.n_seqs + QB_PREP_THREADS - 1) / QB_PREP_THREADS;
   const int b0 = min(a.n_seqs, (int)threadIdx.x * per), b1 = min(a.n_seqs, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += qb_span<N>(a, qb_seq(a, b, a.err)).total() * a.g.n_kv_heads;
-  long long inc = mine;
+  long long work = 0, tiles = 0;
+  for (int b = b0; b < b1; ++b) {
+    const QbSpan s = qb_span<N>(a, qb_seq(a, b, a.err));
+    tiles += s.total() * a.g.n_kv_heads;
+    work += (s.total() + (long long)QB_UNIT_WORK * s.n_rt) * a.g.n_kv_heads;
+  }
+  long long inc_w = work, inc_t = tiles;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += o;
+    const long long w = __shfl_up_sync(0xffffffffu, inc_w, d), t = __shfl_up_sync(0xffffffffu, inc_t, d);
+    if (lane >= d) {
+      inc_w += w;
+      inc_t += t;
+    }
   }
-  if (lane == 31) s_warp[warp] = inc;
+  if (lane == 31) {
+    s_warp[0][warp] = inc_w;
+    s_warp[1][warp] = inc_t;
+  }
   __syncthreads();
-  long long at = inc - mine;
-  for (int w = 0; w < warp; ++w) at += s_warp[w];
-  for (int b = b0; b < b1; ++b) {
-    a.ws.tiles[b] = at;
-    at += qb_span<N>(a, qb_seq(a, b, nullptr)).total() * a.g.n_kv_heads;
+  long long at_w = inc_w - work, at_t = inc_t - tiles;
+  for (int w = 0; w < warp; ++w) {
+    at_w += s_warp[0][w];
+    at_t += s_warp[1][w];
   }
-  if (threadIdx.x == QB_PREP_THREADS - 1) a.ws.tiles[a.n_seqs] = at;
+  for (int b = b0; b < b1; ++b) {
+    a.ws.work[b] = at_w;
+    a.ws.tiles[b] = at_t;
+    const QbSpan s = qb_span<N>(a, qb_seq(a, b, nullptr));
+    at_t += s.total() * a.g.n_kv_heads;
+    at_w += (s.total() + (long long)QB_UNIT_WORK * s.n_rt) * a.g.n_kv_heads;
+  }
+  if (threadIdx.x == QB_PREP_THREADS - 1) {
+    a.ws.work[a.n_seqs] = at_w;
+    a.ws.tiles[a.n_seqs] = at_t;
+  }
 }
 
 __device__ __forceinline__ void qb_number_tree(const QbArgs& a, int b, const int32_t* __restrict__ parents,
@@ -530,9 +557,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 }
 template <int C>
 __device__ __forceinline__ void qb_tmem_ld(uint32_t taddr, float (&v)[C]) {
-  static_assert(C == 8 || C == 16, "columns");
-  if constexpr (C == 8) tmem_ld8(taddr, v);
-  else tmem_ld16(taddr, v);
+  static_assert(C == 8 || C % 16 == 0, "columns");
+  if constexpr (C == 8) {
+    tmem_ld8(taddr, v);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; c += 16) tmem_ld16(taddr + c, *reinterpret_cast<float(*)[16]>(v + c));
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -601,13 +632,13 @@ __device__ __forceinline__ bool qb_vote(int id, bool p) {
 enum { QB_C_SK, QB_C_KZ, QB_C_LS, QB_C_INV, QB_C_ZC };
 
 // Register shares by role (a thread; 0: as launched): keys, values, softmax, accumulation, copies and MMA issue.  The
-// 64-row tile: 32 warps launched with 64 (sum 4 x 40 + 4 x 48 + 16 x 72 + 4 x 96 + 4 x 40 = 32 x 64); the 32-row tile: 24
-// with 80 (4 x 56 + 4 x 56 + 8 x 104 + 4 x 96 + 4 x 56 = 1888 <= 24 x 80).
+// 24 warps are launched with 80; the 64-row tile: 4 x 40 + 4 x 48 + 8 x 128 + 4 x 96 + 4 x 40 = 1920 = 24 x 80; the 32-row
+// tile: 4 x 56 + 4 x 56 + 8 x 104 + 4 x 96 + 4 x 56 = 1888.
 struct QbRegisters {
   int keys, values, softmax, acc, misc;
 };
 __host__ __device__ constexpr QbRegisters qb_shares(int n) {
-  return n == 64 ? QbRegisters{40, 48, 72, 96, 40} : n == 32 ? QbRegisters{56, 56, 104, 96, 56} : QbRegisters{0, 0, 0, 0, 0};
+  return n == 64 ? QbRegisters{40, 48, 128, 96, 40} : n == 32 ? QbRegisters{56, 56, 104, 96, 56} : QbRegisters{0, 0, 0, 0, 0};
 }
 
 // Register shares of a group of four warps (the block's total stays what it was launched with).
@@ -624,13 +655,15 @@ struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) int tin[2][N];
   alignas(16) float neg_m[2][N];    // -M, 0 at first
   alignas(16) float scale[4][N];    // factors of the accumulated numerator for tile i (i % 4), where flagged
-  alignas(16) int moved[4][qb_groups(N)];            // per group: whether tile i (i % 4) moved a reference
-  alignas(16) float red[qb_groups(N)][4][16];        // per group: the rows' maxima per warp
-  alignas(8) float delta[qb_groups(N)][16];          // per group: how far the references moved
+  alignas(8) int moved[4][QB_GROUPS];            // per group: whether tile i (i % 4) moved a reference
+  alignas(16) float red[QB_GROUPS][4][32];        // per group: the rows' maxima per warp
+  alignas(8) float delta[QB_GROUPS][32];          // per group: how far the references moved
   alignas(16) float tok[4][5][QB_TOK];  // constants of tile i (i % 4): see QB_C_*
   alignas(16) float lsum[4][N];
   alignas(16) float zsum[4][N];
   alignas(16) QbUnit unit[QB_UNITS];
+  QbUnit first;
+  alignas(8) long long tiles_before[2];  // the slice's two ends
   float unscale[2];                 // what the products of key codes and queries are scaled back by
   float qmax[2][4];
   float row_z[N], row_f[N];         // of the unit being written out
@@ -652,10 +685,10 @@ static_assert(offsetof(QbShared<16>, neg_m) % 16 == 0 && offsetof(QbShared<16>, 
               "vector reads");
 
 template <int N>
-__global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
-  constexpr int NG = qb_groups(N), NH = N / NG;  // groups of softmax warps, rows of a group
+__global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
+  constexpr int NG = QB_GROUPS, NH = N / NG;  // groups of softmax warps, rows of a group
   constexpr int W_ACC = 8 + 4 * NG, W_COPY = W_ACC + 4, W_MMA = W_COPY + 1;  // first warps of the roles
-  static_assert(NH == 8 || NH == 16, "rows of a softmax group");
+  
   constexpr uint32_t T_K = 0, T_V = 128, T_S = 256, T_O = 384;  // tensor memory columns, two buffers of 64 each
   extern __shared__ uint8_t qb_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(qb_raw) + 1023) & ~uintptr_t(1023));
@@ -699,10 +732,27 @@ __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
   const uint32_t tmem = sh.tmem;
   pdl_wait();
   pdl_launch_dependents();
-  const long long total = a.ws.tiles[a.n_seqs];
-  const QbSlices slices(total, gridDim.x);
-  const long long first = slices.start(blockIdx.x);
-  const int n_tiles = (int)(slices.start(blockIdx.x + 1) - first);
+  {  // the slice's first unit and its tiles
+    const QbSlices slices(a.ws.work[a.n_seqs], gridDim.x);
+    const long long w0 = slices.start(blockIdx.x), w1 = slices.start(blockIdx.x + 1);
+    if (warp < 2) {
+      long long before = 0;
+      if (w1 > w0) {
+        int in;
+        if (warp == 0) {
+          const QbUnit u = qb_locate<N>(a, w0, lane, in, before);
+          if (lane == 0) sh.first = u;
+        } else if (w1 < a.ws.work[a.n_seqs]) {
+          qb_locate<N>(a, w1, lane, in, before);
+        } else {
+          before = a.ws.tiles[a.n_seqs];
+        }
+      }
+      if (lane == 0) sh.tiles_before[warp] = before;
+    }
+    __syncthreads();
+  }
+  const int n_tiles = (int)(sh.tiles_before[1] - sh.tiles_before[0]);
 
   // warp-uniform bounded wait, kept short (it stands in many places); a role that gives up ends, and with
   // it, in time, the others
@@ -1150,7 +1200,7 @@ __global__ void __launch_bounds__(qb_threads(N), 1) qb_attend_kernel(QbArgs a) {
     } else if (warp == W_COPY) {
       qb_registers<qb_shares(N).misc, false>();
       // ---- page copies, and the list of units one ahead of them ----
-      QbUnit u = qb_locate<N>(a, first, lane), ahead;
+      QbUnit u = sh.first, ahead;
       long long left = n_tiles;
       auto publish = [&](int un, QbUnit v, long long room) {
         if (room <= 0) v.t0 = v.t1 = 0;
@@ -1269,19 +1319,20 @@ constexpr int QB_JOIN_ROWS = 8;  // a warp a row
 template <int N>
 __global__ void __launch_bounds__(32 * QB_JOIN_ROWS) qb_combine_kernel(QbArgs a, int grid) {
   const int lane = threadIdx.x & 31, r = blockIdx.y * QB_JOIN_ROWS + (threadIdx.x >> 5);
-  // the list of tiles is complete: the attention's blocks waited for it before they let this grid start
-  const long long total = a.ws.tiles[a.n_seqs];
-  const QbSlices slices(total, grid);
+  // the list of work is complete: the attention's blocks waited for it before they let this grid start
+  const QbSlices slices(a.ws.work[a.n_seqs], grid);
   const int k = blockIdx.x;
   const long long start = slices.start(k), end = slices.start(k + 1);
   if (end == start) {
     pdl_wait();  // every block ends after the attention, so that what follows this grid does too
     return;
   }
-  const QbUnit u = qb_locate<N>(a, end - 1, lane);
-  const long long u0 = end - 1 - u.t0, u1 = u0 + u.nt;
+  int in;
+  long long before;
+  const QbUnit u = qb_locate<N>(a, end - 1, lane, in, before);
+  const long long u0 = end - 1 - in + QB_UNIT_WORK, u1 = u0 + u.nt;  // the work of its tiles
   const int R = u.rt * N + r, tk = R >> a.gqa_shift;
-  if (u1 <= end || u0 < start || tk >= u.n) {
+  if (u1 <= end || u0 < start || u0 >= end || tk >= u.n) {
     pdl_wait();
     return;
   }
@@ -1347,7 +1398,7 @@ static cudaError_t qb_launch(const QbArgs& a, const int32_t* parents, const void
   blocks += 1 + (a.mode == QB_TREE ? a.n_seqs : 0);
   qb_prepare_kernel<N><<<(unsigned)blocks, QB_PREP_THREADS, 0, s>>>(a, parents, q, dtype, rot, chunks);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = qb_launch_pdl(qb_attend_kernel<N>, dim3(grid), qb_threads(N), qb_smem_bytes(N), s, a)) != cudaSuccess) return e;
+  if ((e = qb_launch_pdl(qb_attend_kernel<N>, dim3(grid), QB_THREADS, qb_smem_bytes(N), s, a)) != cudaSuccess) return e;
   return qb_launch_pdl(qb_combine_kernel<N>, dim3(grid, N / QB_JOIN_ROWS), 32 * QB_JOIN_ROWS, 0, s, a, grid);
 }
 
