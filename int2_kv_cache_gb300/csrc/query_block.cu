@@ -27,8 +27,8 @@
 // Softmax weights are kept as w = 2^(a + log2 s - M) directly, p = w / s: fp16 then
 // holds w whatever the value scales are (a constant group, s = 0, takes the
 // smallest fp16 as s: its codes are 0 and mid compensates exactly).  M is a lazy
-// reference, the maximum of the first tile, moved only when a weight would pass
-// 2^14: one vote a tile, and most units never move it again.
+// reference, set from the maximum of the first tile and moved only when a weight
+// would pass fp16's range: one vote a tile, and most units never move it again.
 //
 // A CTA (one per SM, persistent over an equal slice of all tiles):
 //   4 + 4 warps  expand the codes of a tile into tensor memory: a thread owns a token
@@ -57,7 +57,9 @@ constexpr int QB_STAGE_BYTES = QB_TOK * 72;
 constexpr int QB_PBUF = QB_TOK * 128;             // one half of W^T: 128 rows of 128 bytes (64 fp16 columns)
 constexpr int QB_UNITS = 4;                       // ring of unit descriptors
 constexpr int QB_UNIT_WORK = 3;                   // what starting and ending a unit costs, in tiles (measured: 5 us and 1.6 us)
-constexpr float QB_TRIGGER = 14.f;                // the reference moves to the running maximum when a weight would pass 2^14
+// Weights: the running maximum is put at 2^6 (64 times further from fp16's smallest step than at 1: the error of a readout
+// 2e-6 -> 6e-7), and again whenever a weight would pass 2^15.5.
+constexpr float QB_LIFT = 6.f, QB_TRIGGER = 15.5f;
 
 constexpr int QB_GROUPS = 2;                      // groups of four softmax warps, half of the rows each
 // Keys (4 warps), values (4), softmax, accumulation (4), copies, MMA issue and two idle warps: register shares go by four.
@@ -424,7 +426,8 @@ __device__ __forceinline__ void qb_rotate_dense(const QbArgs& a, int h, int slic
           for (int e = 0; e < RUN; ++e)
             in[m][i][c][e] = __ldg(static_cast<const uint4*>(q) + (o[m][i] + 32 * c + 8 * t) / (F32 ? 4 : 8) + e);
       }
-    float d[MT][2][4] = {};
+    // the leading products in two sums of four steps, the others in a third: added in fp32 (the tensor cores truncate)
+    float d[3][MT][2][4] = {};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t x[MT][F32 ? 3 : 1][4];
@@ -456,15 +459,15 @@ __device__ __forceinline__ void qb_rotate_dense(const QbArgs& a, int h, int slic
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           if constexpr (F32) {
-            qb_mma_bf16(d[m][n], x[m][2], b[0]);
-            qb_mma_bf16(d[m][n], x[m][1], b[1]);
-            qb_mma_bf16(d[m][n], x[m][0], b[2]);
-            qb_mma_bf16(d[m][n], x[m][1], b[0]);
+            qb_mma_bf16(d[2][m][n], x[m][2], b[0]);
+            qb_mma_bf16(d[2][m][n], x[m][1], b[1]);
+            qb_mma_bf16(d[2][m][n], x[m][0], b[2]);
+            qb_mma_bf16(d[2][m][n], x[m][1], b[0]);
           } else {
-            qb_mma_bf16(d[m][n], x[m][0], b[2]);
+            qb_mma_bf16(d[2][m][n], x[m][0], b[2]);
           }
-          qb_mma_bf16(d[m][n], x[m][0], b[1]);
-          qb_mma_bf16(d[m][n], x[m][0], b[0]);
+          qb_mma_bf16(d[2][m][n], x[m][0], b[1]);
+          qb_mma_bf16(d[k >> 2][m][n], x[m][0], b[0]);
         }
       }
     }
@@ -476,7 +479,8 @@ __device__ __forceinline__ void qb_rotate_dense(const QbArgs& a, int h, int slic
         for (int i = 0; i < 2; ++i)
           if ((int)r0 + 16 * MT * rg + 16 * m + 8 * i + g < rows)
             *reinterpret_cast<float2*>(a.ws.q + o[m][i] + QB_ROT_COLS * slice + 16 * cg + 8 * n + 2 * t) =
-                make_float2(d[m][n][2 * i] * QB_SCALE, d[m][n][2 * i + 1] * QB_SCALE);
+                make_float2((d[0][m][n][2 * i] + (d[1][m][n][2 * i] + d[2][m][n][2 * i])) * QB_SCALE,
+                            (d[0][m][n][2 * i + 1] + (d[1][m][n][2 * i + 1] + d[2][m][n][2 * i + 1])) * QB_SCALE);
   }
 }
 
@@ -567,25 +571,18 @@ __device__ __forceinline__ void qb_tmem_ld(uint32_t taddr, float (&v)[C]) {
 }
 
 // ---------------------------------------------------------------------------
-// Expansion of 2-bit codes, both 16-bit halves of a register at once.
-// Keys: field f (bits 2f, 2f + 1 of a half) masked in place is the subnormal fp16
-// c * 2^(qb_bit(f) - 24) - one instruction a register; fields that straddle the
-// exponent bits are taken from the byte-swapped halves.  The powers of two are
-// compensated in the queries (exactly).  The queries' signs are mixed, so codes that
-// are not centred cost the sums nothing.
-// Values: the weights are positive, so the codes are centred: a field masked into the
-// mantissa of 2^k + c (exact), from which 2^k + 1.5 is subtracted (exact).
+// Expansion of 2-bit codes, both 16-bit halves of a register at once, as fp16 c - 1.5:
+// a field (bits 2f, 2f + 1 of a half) masked into the mantissa of 2^k + c (exact), from
+// which 2^k + 1.5 is subtracted (exact).  Fields that would straddle the exponent bits
+// are taken from the byte-swapped halves (keys) or rotated (values).  Keys as plain c, a
+// subnormal c 2^(bit - 24) without the subtraction, ran as fast but cost precision in the
+// scores (readout error 1.6e-6 instead of 5e-7).
 // ---------------------------------------------------------------------------
 __host__ __device__ constexpr int qb_bit(int f) { return f == 0 ? 8 : f <= 4 ? 2 * f : 2 * f - 8; }  // 2, 4, 6 or 8
-__host__ __device__ constexpr bool qb_swapped(int f) { return f == 0 || f >= 5; }
 __device__ __forceinline__ uint32_t qb_swap(uint32_t x) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %1, 0x2301;" : "=r"(d) : "r"(x));
   return d;
-}
-template <int F>
-__device__ __forceinline__ uint32_t qb_key_field(uint32_t x, uint32_t x_swapped) {
-  return (qb_swapped(F) ? x_swapped : x) & (0x00030003u << qb_bit(F));
 }
 // The field at bits BIT, BIT + 1 as c - 1.5.
 template <int BIT>
@@ -618,7 +615,7 @@ __device__ __forceinline__ uint32_t qb_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// A token's constants: key scale and zero, log2 of the value scale, its reciprocal, value mid over value scale.
+// A token's constants: key scale and mid, log2 of the value scale, its reciprocal, value mid over value scale.
 // A vote of four warps at hardware barrier `id`.
 __device__ __forceinline__ bool qb_vote(int id, bool p) {
   uint32_t any;
@@ -629,7 +626,7 @@ __device__ __forceinline__ bool qb_vote(int id, bool p) {
       : "memory");
   return any != 0;
 }
-enum { QB_C_SK, QB_C_KZ, QB_C_LS, QB_C_INV, QB_C_ZC };
+enum { QB_C_SK, QB_C_KMID, QB_C_LS, QB_C_INV, QB_C_ZC };
 
 // Register shares by role (a thread; 0: as launched): keys, values, softmax, accumulation, copies and MMA issue.  The
 // 24 warps are launched with 80; the 64-row tile: 4 x 40 + 4 x 48 + 8 x 128 + 4 x 96 + 4 x 40 = 1920 = 24 x 80; the 32-row
@@ -803,7 +800,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         if (i >= 2 && !wait(&sh.s_done[buf], (i >> 1) - 1)) break;
         float(*c)[QB_TOK] = sh.tok[i & 3];
         c[QB_C_SK][tok] = km.x;
-        c[QB_C_KZ][tok] = km.y;
+        c[QB_C_KMID][tok] = fmaf(1.5f, km.x, km.y);
         c[QB_C_LS][tok] = ls;
         c[QB_C_INV][tok] = inv;
         c[QB_C_ZC][tok] = zc;
@@ -816,14 +813,14 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t x = e ? w.y : w.x, y = qb_swap(x);
-            r[8 * e + 0] = qb_key_field<0>(x, y);
-            r[8 * e + 1] = qb_key_field<1>(x, y);
-            r[8 * e + 2] = qb_key_field<2>(x, y);
-            r[8 * e + 3] = qb_key_field<3>(x, y);
-            r[8 * e + 4] = qb_key_field<4>(x, y);
-            r[8 * e + 5] = qb_key_field<5>(x, y);
-            r[8 * e + 6] = qb_key_field<6>(x, y);
-            r[8 * e + 7] = qb_key_field<7>(x, y);
+            r[8 * e + 0] = qb_centred<qb_bit(0)>(y);
+            r[8 * e + 1] = qb_centred<qb_bit(1)>(x);
+            r[8 * e + 2] = qb_centred<qb_bit(2)>(x);
+            r[8 * e + 3] = qb_centred<qb_bit(3)>(x);
+            r[8 * e + 4] = qb_centred<qb_bit(4)>(x);
+            r[8 * e + 5] = qb_centred<qb_bit(5)>(y);
+            r[8 * e + 6] = qb_centred<qb_bit(6)>(y);
+            r[8 * e + 7] = qb_centred<qb_bit(7)>(y);
           }
           tmem_st16(tmem + lanes + T_K + 64 * buf + 16 * k, r);
         }
@@ -936,9 +933,9 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           }
           tc_fence_after();
           const float(*tc)[QB_TOK] = sh.tok[i & 3];
-          const float sk = tc[QB_C_SK][tok] * unscale, kz = tc[QB_C_KZ][tok], ls = tc[QB_C_LS][tok],
+          const float sk = tc[QB_C_SK][tok] * unscale, kmid = tc[QB_C_KMID][tok], ls = tc[QB_C_LS][tok],
                       inv = tc[QB_C_INV][tok], zc = tc[QB_C_ZC][tok];
-          const uint64_t sk2 = f2pk(sk, sk), kz2 = f2pk(kz, kz), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
+          const uint64_t sk2 = f2pk(sk, sk), kmid2 = f2pk(kmid, kmid), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
                          zc2 = f2pk(zc, zc);
           uint8_t* p_hi = s_p + (2 * buf) * QB_PBUF + tok * 128;
           const uint32_t scores = tmem + lanes + T_S + 64 * buf + col0;
@@ -950,8 +947,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           for (int j = 0; j < NH; j += 4) {
             const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col0 + j);
             const float4 nm = *reinterpret_cast<const float4*>(s_neg_m + col0 + j);
-            const uint64_t u0 = f2fma(kz2, f2pk(sq.x, sq.y), f2add(f2pk(nm.x, nm.y), ls2));
-            const uint64_t u1 = f2fma(kz2, f2pk(sq.z, sq.w), f2add(f2pk(nm.z, nm.w), ls2));
+            const uint64_t u0 = f2fma(kmid2, f2pk(sq.x, sq.y), f2add(f2pk(nm.x, nm.y), ls2));
+            const uint64_t u1 = f2fma(kmid2, f2pk(sq.z, sq.w), f2add(f2pk(nm.z, nm.w), ls2));
             const float2 d0 = f2up(f2fma(sk2, f2pk(x[j], x[j + 1]), u0));
             const float2 d1 = f2up(f2fma(sk2, f2pk(x[j + 2], x[j + 3]), u1));
             x[j] = d0.x; x[j + 1] = d0.y; x[j + 2] = d1.x; x[j + 3] = d1.y;
@@ -977,7 +974,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             if (tok < NH) {
               const float m = fmaxf(fmaxf(sh.red[group][0][tok], sh.red[group][1][tok]),
                                     fmaxf(sh.red[group][2][tok], sh.red[group][3][tok]));
-              const float by = (unset ? m > -INFINITY : m > 0.f) ? m : 0.f;
+              const float by = (unset ? m > -INFINITY : m > QB_LIFT) ? m - QB_LIFT : 0.f;
               s_neg_m[col0 + tok] -= by;
               sh.delta[group][tok] = by;
               sh.scale[i & 3][col0 + tok] = unset ? 1.f : qb_ex2(-by);  // nothing to scale yet
@@ -1099,8 +1096,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           if (lane == 0) sh.qmax[buf][q4] = m;
           if (!meet()) break;
           m = fmaxf(fmaxf(sh.qmax[buf][0], sh.qmax[buf][1]), fmaxf(sh.qmax[buf][2], sh.qmax[buf][3]));
-          // the largest at 2^8 .. 2^9, times up to 2^6 for the keys' fields
-          const int e = m > 0.f ? min(100, max(-100, 8 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
+          // the largest at 2^13 .. 2^14
+          const int e = m > 0.f ? min(100, max(-100, 13 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
           const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
           uint8_t* dst = s_q + buf * N * 512 + row * 128;
 #pragma unroll
@@ -1109,8 +1106,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int f = 0; f < 8; ++f) {
-              const float up = scale * (float)(1 << (8 - qb_bit(f)));
-              const float x = v[j + f] * up, y = v[j + 8 + f] * up;
+              const float x = v[j + f] * scale, y = v[j + 8 + f] * scale;
               hi[f] = qb_half2(x, y);
               const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[f]));
               lo[f] = qb_half2(x - back.x, y - back.y);
@@ -1129,7 +1125,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             sh.tin[buf][row] =
                 !valid ? 0 : a.mode == QB_TREE ? a.ws.tree[next.c0 + tk].x : a.mode == QB_CHAIN ? tk : 0;
           }
-          if (wt == 0) sh.unscale[buf] = __uint_as_float((uint32_t)(127 + 16 - e) << 23);
+          if (wt == 0) sh.unscale[buf] = __uint_as_float((uint32_t)(127 - e) << 23);
           fence_proxy_async();
           arrive(&sh.q_ready[buf]);
         }
@@ -1388,10 +1384,10 @@ static cudaError_t qb_launch(const QbArgs& a, const int32_t* parents, const void
   const long long rows = (long long)a.n_total * a.n_q_heads;
   long long blocks = (rows + QB_PREP_THREADS / 32 - 1) / (QB_PREP_THREADS / 32);
   int chunks = 1;
-  if (rot.kind == KVQ_ROT_DENSE) {  // about four blocks an SM, each with R's limbs split once
+  if (rot.kind == KVQ_ROT_DENSE) {  // at most three blocks an SM (their registers), one wave, each with R's limbs split once
     const int per_chunk = a.g.n_kv_heads * (D / QB_ROT_COLS);
     const int tile = qb_rot_rows(dtype == KVQ_F32);
-    const long long tiles = ((long long)a.n_total * a.gqa + tile - 1) / tile, most = 4 * grid / per_chunk;
+    const long long tiles = ((long long)a.n_total * a.gqa + tile - 1) / tile, most = 3 * grid / per_chunk;
     chunks = (int)std::max<long long>(1, std::min(tiles, most));
     blocks = (long long)per_chunk * chunks;
   }
