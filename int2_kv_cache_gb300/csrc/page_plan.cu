@@ -12,20 +12,24 @@
 // num_blocks is checked), so every item is independent once the sums exist.
 // Bound: latency (a 256-request step moves a few KB).  Up to PLAN_SMALL sequences
 // every CTA forms the prefix sums itself in shared memory and the plan is one
-// launch; above, a one-CTA scan leaves them in the workspace for a second launch.
+// launch; above, a one-CTA scan leaves them in the workspace for a second launch
+// (8,191 requests took 34 us in two launches).
 //
 // kvq_tree_commit moves the 72-byte records of the accepted drafts down to the
 // first drafts' slots: no arithmetic, so the cache bytes are those that were
 // attended.  One warp owns a (sequence, KV head): it loads up to 32 records into
 // registers before it stores any, and as accepted[i] >= i with both increasing,
 // no store of an earlier batch can hit a later batch's source.
+#include <algorithm>
+
 #include "kvq_internal.cuh"
 
 namespace kvq {
 
-constexpr int PLAN_SMALL = 1024;
-constexpr int PLAN_THREADS = 256;
-constexpr int PLAN_SCAN_THREADS = 1024;
+constexpr int PLAN_SMALL = 16384;       // 3 arrays of 4 bytes: 192 KB of shared memory
+constexpr int PLAN_THREADS = 256;       // up to PLAN_FEW sequences, and in the second launch of two
+constexpr int PLAN_MANY_THREADS = 1024;
+constexpr int PLAN_FEW = 1024;
 
 struct PlanSums {
   long long tok, take, give;
@@ -79,7 +83,8 @@ __device__ __forceinline__ bool plan_feasible(const PlanSums& t, long long head,
 }
 
 // The sequence whose half-open prefix range holds item i: pre[b] <= i < pre[b + 1].
-__device__ __forceinline__ int plan_find(const long long* pre, int n, long long i) {
+template <typename T>
+__device__ __forceinline__ int plan_find(const T* pre, int n, long long i) {
   int lo = 0, hi = n;  // pre[lo] <= i < pre[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -106,45 +111,29 @@ __device__ __forceinline__ int plan_wrap(long long i, int num_blocks) {
   return (int)(i >= num_blocks ? i - num_blocks : i);
 }
 
-// Every item of the plan, grid-strided; tok / take / give: prefix arrays of n_seqs + 1.
-__device__ __forceinline__ void plan_expand(const PlanArgs& a, const long long* tok, const long long* take,
-                                            const long long* give, bool ok, long long head, long long tail) {
+// The plan's items, grid-strided over blockIdx.x; blockIdx.y is their kind, so that the kinds' chains of loads run
+// beside one another.  tok / take / give: prefix arrays of n_seqs + 1.
+enum { PLAN_TOKENS = 0, PLAN_TAKES = 1, PLAN_GIVES = 2, PLAN_KINDS = 3 };
+
+template <typename T>
+__device__ __forceinline__ void plan_tokens(const PlanArgs& a, const T* tok, const T* take, const int* old_lens,
+                                            const PlanSums& total, bool ok, long long head, long long tail) {
   const long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
   if (i0 == 0) {
-    a.ring_out[0] = ok ? head + take[a.n_seqs] : head;
-    a.ring_out[1] = ok ? tail + give[a.n_seqs] : tail;
+    a.ring_out[0] = ok ? head + total.take : head;
+    a.ring_out[1] = ok ? tail + total.give : tail;
   }
   for (long long b = i0; b <= a.n_seqs; b += step) a.cu_new[b] = ok ? (int32_t)tok[b] : 0;
-  if (!ok) {
-    for (long long t = i0; t < a.max_new; t += step) a.slots[t] = -1;
-    return;
-  }
-  const int mask = (1 << a.page_shift) - 1;
-  const int hm = (int)(head % a.num_blocks), tm = (int)(tail % a.num_blocks);
-  for (long long k = i0; k < take[a.n_seqs]; k += step) {
-    const int b = plan_find(take, a.n_seqs, k);
-    const int p0 = (int)(((unsigned)a.old_lens[b] + mask) >> a.page_shift);
-    const int page = a.ring[plan_wrap(hm + k, a.num_blocks)];
-    if ((unsigned)page >= (unsigned)a.num_blocks) flag_error(a.err, ERR_BLOCK_RANGE);
-    a.table[(size_t)b * a.max_blocks + p0 + (int)(k - take[b])] = page;
-  }
-  for (long long k = i0; k < give[a.n_seqs]; k += step) {
-    const int b = plan_find(give, a.n_seqs, k);
-    const int p1 = (int)(((unsigned)a.new_lens[b] + mask) >> a.page_shift);
-    const int page = a.table[(size_t)b * a.max_blocks + p1 + (int)(k - give[b])];
-    if ((unsigned)page >= (unsigned)a.num_blocks) flag_error(a.err, ERR_BLOCK_RANGE);
-    a.ring[plan_wrap(tm + k, a.num_blocks)] = page;
-  }
-  const long long n_tok = tok[a.n_seqs];
+  const int mask = (1 << a.page_shift) - 1, hm = ok ? (int)(head % a.num_blocks) : 0;
   for (long long t = i0; t < a.max_new; t += step) {
     long long slot = -1;
-    if (t < n_tok) {
+    if (ok && t < total.tok) {
       const int b = plan_find(tok, a.n_seqs, t);
-      const int old = a.old_lens[b];
+      const int old = old_lens[b];
       const int pos = old + (int)(t - tok[b]);
       const int p0 = (int)(((unsigned)old + mask) >> a.page_shift), pi = pos >> a.page_shift;
       const int page = pi < p0 ? a.table[(size_t)b * a.max_blocks + pi]
-                               : a.ring[plan_wrap(hm + take[b] + (pi - p0), a.num_blocks)];
+                               : a.ring[plan_wrap((long long)hm + take[b] + (pi - p0), a.num_blocks)];
       if ((unsigned)page < (unsigned)a.num_blocks) slot = ((long long)page << a.page_shift) + (pos & mask);
       else flag_error(a.err, ERR_BLOCK_RANGE);
     }
@@ -152,57 +141,94 @@ __device__ __forceinline__ void plan_expand(const PlanArgs& a, const long long* 
   }
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_small_kernel(PlanArgs a) {
-  __shared__ long long s_pre[3][PLAN_SMALL + 1];
-  __shared__ PlanSums s_warp[PLAN_THREADS / 32];
-  constexpr int PER = PLAN_SMALL / PLAN_THREADS;
+template <typename T>
+__device__ __forceinline__ void plan_takes(const PlanArgs& a, const T* take, const int* old_lens, long long count,
+                                           long long head) {
+  const int mask = (1 << a.page_shift) - 1, hm = (int)(head % a.num_blocks);
+  for (long long k = (long long)blockIdx.x * blockDim.x + threadIdx.x; k < count; k += (long long)gridDim.x * blockDim.x) {
+    const int page = a.ring[plan_wrap(hm + k, a.num_blocks)];
+    const int b = plan_find(take, a.n_seqs, k);
+    const int p0 = (int)(((unsigned)old_lens[b] + mask) >> a.page_shift);
+    if ((unsigned)page >= (unsigned)a.num_blocks) flag_error(a.err, ERR_BLOCK_RANGE);
+    a.table[(size_t)b * a.max_blocks + p0 + (int)(k - take[b])] = page;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void plan_gives(const PlanArgs& a, const T* give, const int* new_lens, long long count,
+                                           long long tail) {
+  const int mask = (1 << a.page_shift) - 1, tm = (int)(tail % a.num_blocks);
+  for (long long k = (long long)blockIdx.x * blockDim.x + threadIdx.x; k < count; k += (long long)gridDim.x * blockDim.x) {
+    const int b = plan_find(give, a.n_seqs, k);
+    const int p1 = (int)(((unsigned)new_lens[b] + mask) >> a.page_shift);
+    const int page = a.table[(size_t)b * a.max_blocks + p1 + (int)(k - give[b])];
+    if ((unsigned)page >= (unsigned)a.num_blocks) flag_error(a.err, ERR_BLOCK_RANGE);
+    a.ring[plan_wrap(tm + k, a.num_blocks)] = page;
+  }
+}
+
+// One launch: every CTA holds what its kind of item needs in shared memory: the sums in 32 bits (those of a plan that
+// can be carried out fit: tokens <= max_new, pages <= num_blocks; of another only the verdict, taken in 64 bits, is used)
+// and the lengths.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) plan_small_kernel(PlanArgs a) {
+  extern __shared__ int s_pre[];
+  __shared__ PlanSums s_warp[THREADS / 32];
+  const int kind = blockIdx.y;
+  int *s_items = s_pre, *s_lens = s_pre + a.n_seqs + 1, *s_take = s_pre + 2 * (a.n_seqs + 1);
+  constexpr int PER = THREADS == PLAN_THREADS ? PLAN_FEW / PLAN_THREADS : PLAN_SMALL / PLAN_MANY_THREADS;
+  const int per = (a.n_seqs + THREADS - 1) / THREADS;
+  const int b0 = min(a.n_seqs, (int)threadIdx.x * per), b1 = min(a.n_seqs, b0 + per);
   const long long max_tokens = (long long)a.max_blocks << a.page_shift;
-  PlanSums v[PER], mine{0, 0, 0};
+  const long long head = a.ring_in[0], tail = a.ring_in[1];
+  int o[PER], n[PER];  // a thread's run of sequences, its loads in flight together
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    o[i] = b0 + i < b1 ? a.old_lens[b0 + i] : 0;
+    n[i] = b0 + i < b1 ? a.new_lens[b0 + i] : 0;
+  }
+  PlanSums mine{0, 0, 0};
   bool ok = true;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int b = threadIdx.x * PER + i;
-    v[i] = b < a.n_seqs ? plan_counts(a.old_lens[b], a.new_lens[b], a.page_shift, max_tokens, ok) : PlanSums{0, 0, 0};
-    mine = plan_add(mine, v[i]);
-  }
-  const long long head = a.ring_in[0], tail = a.ring_in[1];
+  for (int i = 0; i < PER; ++i) mine = plan_add(mine, plan_counts(o[i], n[i], a.page_shift, max_tokens, ok));
   PlanSums at;
-  const PlanSums total = plan_scan<PLAN_THREADS>(mine, at, s_warp);
+  const PlanSums total = plan_scan<THREADS>(mine, at, s_warp);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int b = threadIdx.x * PER + i;
-    if (b < a.n_seqs) {
-      s_pre[0][b] = at.tok;
-      s_pre[1][b] = at.take;
-      s_pre[2][b] = at.give;
+    if (b0 + i < b1) {
+      s_items[b0 + i] = (int)(kind == PLAN_TOKENS ? at.tok : kind == PLAN_TAKES ? at.take : at.give);
+      s_lens[b0 + i] = kind == PLAN_GIVES ? n[i] : o[i];
+      if (kind == PLAN_TOKENS) s_take[b0 + i] = (int)at.take;
     }
-    at = plan_add(at, v[i]);
+    at = plan_add(at, plan_counts(o[i], n[i], a.page_shift, max_tokens, ok));
   }
-  if (threadIdx.x == 0) {
-    s_pre[0][a.n_seqs] = total.tok;
-    s_pre[1][a.n_seqs] = total.take;
-    s_pre[2][a.n_seqs] = total.give;
-  }
+  if (threadIdx.x == 0) s_items[a.n_seqs] = (int)(kind == PLAN_TOKENS ? total.tok : kind == PLAN_TAKES ? total.take : total.give);
   ok = __syncthreads_and(ok) && plan_feasible(total, head, tail, a.num_blocks, a.max_new);
-  if (!ok && blockIdx.x == 0 && threadIdx.x == 0) flag_error(a.err, ERR_PLAN);
-  plan_expand(a, s_pre[0], s_pre[1], s_pre[2], ok, head, tail);
+  if (kind == PLAN_TOKENS) {
+    if (!ok && blockIdx.x == 0 && threadIdx.x == 0) flag_error(a.err, ERR_PLAN);
+    plan_tokens(a, s_items, s_take, s_lens, total, ok, head, tail);
+  } else if (ok && kind == PLAN_TAKES) {
+    plan_takes(a, s_items, s_lens, total.take, head);
+  } else if (ok) {
+    plan_gives(a, s_items, s_lens, total.give, tail);
+  }
 }
 
 // Workspace of the two-launch plan: three prefix arrays of n_seqs + 1, then 0 / 1 (feasible).
 size_t plan_workspace_bytes(int n_seqs) { return ((size_t)3 * (n_seqs + 1) + 1) * sizeof(long long); }
 
-__global__ void __launch_bounds__(PLAN_SCAN_THREADS) plan_scan_kernel(PlanArgs a, long long* ws) {
-  __shared__ PlanSums s_warp[PLAN_SCAN_THREADS / 32];
+__global__ void __launch_bounds__(PLAN_MANY_THREADS) plan_scan_kernel(PlanArgs a, long long* ws) {
+  __shared__ PlanSums s_warp[PLAN_MANY_THREADS / 32];
   long long *tok = ws, *take = ws + a.n_seqs + 1, *give = ws + 2 * ((size_t)a.n_seqs + 1);
   const long long max_tokens = (long long)a.max_blocks << a.page_shift;
-  const int per = (a.n_seqs + PLAN_SCAN_THREADS - 1) / PLAN_SCAN_THREADS;
+  const int per = (a.n_seqs + PLAN_MANY_THREADS - 1) / PLAN_MANY_THREADS;
   const int b0 = min(a.n_seqs, (int)threadIdx.x * per), b1 = min(a.n_seqs, b0 + per);
   bool ok = true;
   PlanSums mine{0, 0, 0};
   for (int b = b0; b < b1; ++b)
     mine = plan_add(mine, plan_counts(a.old_lens[b], a.new_lens[b], a.page_shift, max_tokens, ok));
   PlanSums at;
-  const PlanSums total = plan_scan<PLAN_SCAN_THREADS>(mine, at, s_warp);
+  const PlanSums total = plan_scan<PLAN_MANY_THREADS>(mine, at, s_warp);
   for (int b = b0; b < b1; ++b) {
     tok[b] = at.tok;
     take[b] = at.take;
@@ -220,8 +246,12 @@ __global__ void __launch_bounds__(PLAN_SCAN_THREADS) plan_scan_kernel(PlanArgs a
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) plan_expand_kernel(PlanArgs a, const long long* ws) {
-  plan_expand(a, ws, ws + a.n_seqs + 1, ws + 2 * ((size_t)a.n_seqs + 1), ws[3 * ((size_t)a.n_seqs + 1)] != 0,
-              a.ring_in[0], a.ring_in[1]);
+  const long long *tok = ws, *take = ws + a.n_seqs + 1, *give = ws + 2 * ((size_t)a.n_seqs + 1);
+  const bool ok = ws[3 * ((size_t)a.n_seqs + 1)] != 0;
+  const PlanSums total{tok[a.n_seqs], take[a.n_seqs], give[a.n_seqs]};
+  if (blockIdx.y == PLAN_TOKENS) plan_tokens(a, tok, take, a.old_lens, total, ok, a.ring_in[0], a.ring_in[1]);
+  else if (ok && blockIdx.y == PLAN_TAKES) plan_takes(a, take, a.old_lens, total.take, a.ring_in[0]);
+  else if (ok) plan_gives(a, give, a.new_lens, total.give, a.ring_in[1]);
 }
 
 cudaError_t launch_plan_pages(const PageGeom& g, int n_seqs, const int32_t* old_lens, const int32_t* new_lens,
@@ -231,13 +261,19 @@ cudaError_t launch_plan_pages(const PageGeom& g, int n_seqs, const int32_t* old_
                    table, ring, reinterpret_cast<const long long*>(ring_in), reinterpret_cast<long long*>(ring_out),
                    cu_new, reinterpret_cast<long long*>(slots), err};
   const long long items = max_new > n_seqs ? max_new : n_seqs + 1;
-  const long long want = (items + PLAN_THREADS - 1) / PLAN_THREADS, most = 4ll * device_sm_count();
-  const int grid = (int)(want < most ? want : most);
-  if (n_seqs <= PLAN_SMALL) {
-    plan_small_kernel<<<grid, PLAN_THREADS, 0, s>>>(a);
+  const int sms = device_sm_count();
+  auto blocks = [&](int threads, int most) { return dim3((unsigned)std::min<long long>((items + threads - 1) / threads, most), PLAN_KINDS); };
+  const int smem = 3 * (n_seqs + 1) * (int)sizeof(int);
+  if (n_seqs <= PLAN_FEW) {
+    plan_small_kernel<PLAN_THREADS><<<blocks(PLAN_THREADS, 2 * sms), PLAN_THREADS, smem, s>>>(a);
+  } else if (n_seqs <= PLAN_SMALL) {
+    static std::atomic<unsigned long long> attr{0};  // per device
+    const cudaError_t e = smem_limit_once(attr, plan_small_kernel<PLAN_MANY_THREADS>, 3 * (PLAN_SMALL + 1) * (int)sizeof(int));
+    if (e != cudaSuccess) return e;
+    plan_small_kernel<PLAN_MANY_THREADS><<<blocks(PLAN_MANY_THREADS, std::max(1, sms / PLAN_KINDS)), PLAN_MANY_THREADS, smem, s>>>(a);
   } else {
-    plan_scan_kernel<<<1, PLAN_SCAN_THREADS, 0, s>>>(a, static_cast<long long*>(ws));
-    plan_expand_kernel<<<grid, PLAN_THREADS, 0, s>>>(a, static_cast<const long long*>(ws));
+    plan_scan_kernel<<<1, PLAN_MANY_THREADS, 0, s>>>(a, static_cast<long long*>(ws));
+    plan_expand_kernel<<<blocks(PLAN_THREADS, 4 * sms), PLAN_THREADS, 0, s>>>(a, static_cast<const long long*>(ws));
   }
   return cudaGetLastError();
 }

@@ -57,9 +57,9 @@ constexpr int QB_STAGE_BYTES = QB_TOK * 72;
 constexpr int QB_PBUF = QB_TOK * 128;             // one half of W^T: 128 rows of 128 bytes (64 fp16 columns)
 constexpr int QB_UNITS = 4;                       // ring of unit descriptors
 constexpr int QB_UNIT_WORK = 3;                   // what starting and ending a unit costs, in tiles (measured: 5 us and 1.6 us)
-// Weights: the running maximum is put at 2^6 (64 times further from fp16's smallest step than at 1: the error of a readout
-// 2e-6 -> 6e-7), and again whenever a weight would pass 2^15.5.
-constexpr float QB_LIFT = 6.f, QB_TRIGGER = 15.5f;
+// Weights: the running maximum is put at 2^3 (further from fp16's smallest step than at 1: readout error 6.5e-7 -> 4.6e-7,
+// the same at 2^6), and again whenever a weight would pass 2^15.5.
+constexpr float QB_LIFT = 3.f, QB_TRIGGER = 15.5f;
 
 constexpr int QB_GROUPS = 2;                      // groups of four softmax warps, half of the rows each
 // Keys (4 warps), values (4), softmax, accumulation (4), copies, MMA issue and two idle warps: register shares go by four.

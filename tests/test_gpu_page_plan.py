@@ -46,7 +46,7 @@ class Pages:
             self.lens = np.asarray(new, np.int64)
 
 
-@pytest.mark.parametrize("n,page", [(1, 16), (5, 8), (1023, 16), (1024, 8), (1025, 16), (5000, 8)])
+@pytest.mark.parametrize("n,page", [(1, 16), (5, 8), (1023, 16), (1024, 8), (1025, 16), (5000, 8), (16384, 8), (16385, 16)])
 def test_plans_over_many_steps(n, page):
     p = Pages(n, n, page, 9, 9 * n + 3)
     for _ in range(6):
@@ -64,7 +64,7 @@ def test_one_long_request_and_none_at_all():
     p.step([1], 1)
 
 
-@pytest.mark.parametrize("n", [3, 1500])
+@pytest.mark.parametrize("n", [3, 1500, 17000])
 def test_refused_plans_change_nothing(n):
     p = Pages(3, n, 8, 4, 3 * n)
     p.step(np.full(n, 17), 17 * n)                                # every page is taken
