@@ -77,6 +77,7 @@ struct QbWs {
   int2* tree;        // [n_total] (tin, size)
   long long* work;   // [n_seqs + 1] running sum of the sequences' work (tiles, and QB_UNIT_WORK a unit)
   long long* tiles;  // [n_seqs + 1] running sum of their tiles
+  int4* join;        // [grid] the unit that starts in a slice and runs past its end: (first draft's row, drafts, row tile * H + head, parts); parts 0: none
   float* part;       // [2 grid][N][130]: numerator [N][128], l [N], M [N]
 };
 
@@ -92,13 +93,15 @@ static size_t qb_layout(void* base, int n_seqs, int n_total, int n_q_heads, int 
   const size_t o_tree = qb_align((size_t)n_total * n_q_heads * D * sizeof(float));
   const size_t o_work = qb_align(o_tree + (size_t)n_total * sizeof(int2));
   const size_t o_tiles = qb_align(o_work + ((size_t)n_seqs + 1) * sizeof(long long));
-  const size_t o_part = qb_align(o_tiles + ((size_t)n_seqs + 1) * sizeof(long long));
+  const size_t o_join = qb_align(o_tiles + ((size_t)n_seqs + 1) * sizeof(long long));
+  const size_t o_part = qb_align(o_join + (size_t)grid * sizeof(int4));
   if (out) {
     char* p = static_cast<char*>(base);
     out->q = reinterpret_cast<float*>(p);
     out->tree = reinterpret_cast<int2*>(p + o_tree);
     out->work = reinterpret_cast<long long*>(p + o_work);
     out->tiles = reinterpret_cast<long long*>(p + o_tiles);
+    out->join = reinterpret_cast<int4*>(p + o_join);
     out->part = reinterpret_cast<float*>(p + o_part);
   }
   return qb_align(o_part + (size_t)2 * grid * rows * (D + 2) * sizeof(float));
@@ -189,24 +192,92 @@ struct QbUnit {
   int t0, t1, nt;     // tiles [t0, t1) of nt in this slice
 };
 
+// The running sums of the sequences' work and tiles, held by a warp.  Of up to QB_FEW sequences it takes them from the
+// inputs itself (a lane a run of them), without waiting for the preparation; of more, from the workspace.
+constexpr int QB_FEW = 128;
+
+template <int N>
+struct QbList {
+  bool few;
+  int b0, b1;               // this lane's run
+  long long work0, tiles0;  // before it
+  long long work, tiles;    // of all
+
+  __device__ __forceinline__ QbList(const QbArgs& a, int lane) : few(a.n_seqs <= QB_FEW) {
+    if (!few) {
+      work = a.ws.work[a.n_seqs];
+      tiles = a.ws.tiles[a.n_seqs];
+      return;
+    }
+    const int per = (a.n_seqs + 31) / 32;
+    b0 = min(a.n_seqs, lane * per);
+    b1 = min(a.n_seqs, b0 + per);
+    work = tiles = 0;
+    for (int b = b0; b < b1; ++b) add(a, qb_span<N>(a, qb_seq(a, b, nullptr)), work, tiles);
+    work0 = -work;
+    tiles0 = -tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long w = __shfl_up_sync(0xffffffffu, work, d), t = __shfl_up_sync(0xffffffffu, tiles, d);
+      if (lane >= d) {
+        work += w;
+        tiles += t;
+      }
+    }
+    work0 += work;
+    tiles0 += tiles;
+    work = __shfl_sync(0xffffffffu, work, 31);
+    tiles = __shfl_sync(0xffffffffu, tiles, 31);
+  }
+  static __device__ __forceinline__ void add(const QbArgs& a, const QbSpan& s, long long& work, long long& tiles) {
+    work += (s.total() + (long long)QB_UNIT_WORK * s.n_rt) * a.g.n_kv_heads;
+    tiles += s.total() * a.g.n_kv_heads;
+  }
+  // The last sequence that starts at or before w (< work), and the sums before it.
+  __device__ __forceinline__ int find(const QbArgs& a, long long w, int lane, long long& at_work, long long& at_tiles) const {
+    if (few) {
+      const int owner = 31 - __clz(__ballot_sync(0xffffffffu, b1 > b0 && work0 <= w));
+      int b = b0;
+      long long bw = work0, bt = tiles0;
+      if (lane == owner) {
+        long long nw = bw, nt = bt;
+        for (int c = b0; c < b1 && nw <= w; ++c) {
+          b = c;
+          bw = nw;
+          bt = nt;
+          add(a, qb_span<N>(a, qb_seq(a, c, nullptr)), nw, nt);
+        }
+      }
+      at_work = __shfl_sync(0xffffffffu, bw, owner);
+      at_tiles = __shfl_sync(0xffffffffu, bt, owner);
+      return __shfl_sync(0xffffffffu, b, owner);
+    }
+    int lo = 0, cnt = a.n_seqs;
+    while (cnt > 1) {
+      const int step = (cnt + 31) / 32, i = lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, i < cnt && a.ws.work[lo + i] <= w);
+      const int k = 31 - __clz(m);
+      lo += k * step;
+      cnt = min(step, cnt - k * step);
+    }
+    at_work = a.ws.work[lo];
+    at_tiles = a.ws.tiles[lo];
+    return lo;
+  }
+};
+
 // The unit that holds the work at `w`, by one warp: u.t0 = the first of its tiles at or after w; `in`: w inside the unit;
 // `before`: the tiles of all that come before w.
 template <int N>
-__device__ __forceinline__ QbUnit qb_locate(const QbArgs& a, long long w, int lane, int& in, long long& before) {
-  int lo = 0, cnt = a.n_seqs;
-  while (cnt > 1) {  // the last sequence that starts at or before w
-    const int step = (cnt + 31) / 32, i = lane * step;
-    const unsigned m = __ballot_sync(0xffffffffu, i < cnt && a.ws.work[lo + i] <= w);
-    const int k = 31 - __clz(m);
-    lo += k * step;
-    cnt = min(step, cnt - k * step);
-  }
+__device__ __forceinline__ QbUnit qb_locate(const QbArgs& a, const QbList<N>& list, long long w, int lane, int& in,
+                                            long long& before) {
+  long long at_work, at_tiles;
   QbUnit u;
-  u.b = lo;
-  const QbSeq q = qb_seq(a, lo, nullptr);
+  u.b = list.find(a, w, lane, at_work, at_tiles);
+  const QbSeq q = qb_seq(a, u.b, nullptr);
   const QbSpan s = qb_span<N>(a, q);
   const int H = a.g.n_kv_heads;
-  const long long rem = w - a.ws.work[lo];
+  const long long rem = w - at_work;
   int j0 = 0, j1 = s.n_rt;
   while (j1 - j0 > 1) {
     const int mid = (j0 + j1) >> 1;
@@ -224,7 +295,7 @@ __device__ __forceinline__ QbUnit qb_locate(const QbArgs& a, long long w, int la
   u.c0 = q.c0;
   u.n = q.n;
   u.len = q.len;
-  before = a.ws.tiles[lo] + s.before(j0) * H + (long long)u.h * u.nt + u.t0;
+  before = at_tiles + s.before(j0) * H + (long long)u.h * u.nt + u.t0;
   return u;
 }
 
@@ -267,9 +338,7 @@ __device__ __forceinline__ void qb_list_tiles(const QbArgs& a) {
   const int b0 = min(a.n_seqs, (int)threadIdx.x * per), b1 = min(a.n_seqs, b0 + per);
   long long work = 0, tiles = 0;
   for (int b = b0; b < b1; ++b) {
-    const QbSpan s = qb_span<N>(a, qb_seq(a, b, a.err));
-    tiles += s.total() * a.g.n_kv_heads;
-    work += (s.total() + (long long)QB_UNIT_WORK * s.n_rt) * a.g.n_kv_heads;
+    QbList<N>::add(a, qb_span<N>(a, qb_seq(a, b, a.err)), work, tiles);
   }
   long long inc_w = work, inc_t = tiles;
 #pragma unroll
@@ -293,9 +362,7 @@ __device__ __forceinline__ void qb_list_tiles(const QbArgs& a) {
   for (int b = b0; b < b1; ++b) {
     a.ws.work[b] = at_w;
     a.ws.tiles[b] = at_t;
-    const QbSpan s = qb_span<N>(a, qb_seq(a, b, nullptr));
-    at_t += s.total() * a.g.n_kv_heads;
-    at_w += (s.total() + (long long)QB_UNIT_WORK * s.n_rt) * a.g.n_kv_heads;
+    QbList<N>::add(a, qb_span<N>(a, qb_seq(a, b, nullptr)), at_w, at_t);
   }
   if (threadIdx.x == QB_PREP_THREADS - 1) {
     a.ws.work[a.n_seqs] = at_w;
@@ -661,6 +728,7 @@ struct QbShared {  // alignas: read as 16-byte vectors
   alignas(16) QbUnit unit[QB_UNITS];
   QbUnit first;
   alignas(8) long long tiles_before[2];  // the slice's two ends
+  long long work;                        // of all slices
   float unscale[2];                 // what the products of key codes and queries are scaled back by
   float qmax[2][4];
   float row_z[N], row_f[N];         // of the unit being written out
@@ -685,7 +753,6 @@ template <int N>
 __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
   constexpr int NG = QB_GROUPS, NH = N / NG;  // groups of softmax warps, rows of a group
   constexpr int W_ACC = 8 + 4 * NG, W_COPY = W_ACC + 4, W_MMA = W_COPY + 1;  // first warps of the roles
-  
   constexpr uint32_t T_K = 0, T_V = 128, T_S = 256, T_O = 384;  // tensor memory columns, two buffers of 64 each
   extern __shared__ uint8_t qb_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(qb_raw) + 1023) & ~uintptr_t(1023));
@@ -697,7 +764,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr unsigned FULLM = 0xffffffffu;
 
-  if (tid == 0) {
+  // Up to QB_FEW sequences the list of work, the pages and their expansion need nothing of the preparation: only the
+  // warps that read its queries and trees wait for it.
+  if (a.n_seqs > QB_FEW) pdl_wait();
+  if (tid == 32) {
     for (int i = 0; i < QB_STAGES; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 4 + 4);
@@ -723,32 +793,32 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
+  if (warp == 2 || warp == 3) {  // the slice's first unit and its tiles
+    const QbList<N> list(a, lane);
+    const QbSlices slices(list.work, gridDim.x);
+    const long long w0 = slices.start(blockIdx.x), w1 = slices.start(blockIdx.x + 1);
+    long long before = 0;
+    if (w1 > w0) {
+      int in;
+      if (warp == 2) {
+        const QbUnit u = qb_locate<N>(a, list, w0, lane, in, before);
+        if (lane == 0) sh.first = u;
+      } else if (w1 < list.work) {
+        qb_locate<N>(a, list, w1, lane, in, before);
+      } else {
+        before = list.tiles;
+      }
+    }
+    if (lane == 0) {
+      sh.tiles_before[warp - 2] = before;
+      sh.work = list.work;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  pdl_wait();
   pdl_launch_dependents();
-  {  // the slice's first unit and its tiles
-    const QbSlices slices(a.ws.work[a.n_seqs], gridDim.x);
-    const long long w0 = slices.start(blockIdx.x), w1 = slices.start(blockIdx.x + 1);
-    if (warp < 2) {
-      long long before = 0;
-      if (w1 > w0) {
-        int in;
-        if (warp == 0) {
-          const QbUnit u = qb_locate<N>(a, w0, lane, in, before);
-          if (lane == 0) sh.first = u;
-        } else if (w1 < a.ws.work[a.n_seqs]) {
-          qb_locate<N>(a, w1, lane, in, before);
-        } else {
-          before = a.ws.tiles[a.n_seqs];
-        }
-      }
-      if (lane == 0) sh.tiles_before[warp] = before;
-    }
-    __syncthreads();
-  }
+  const uint32_t tmem = sh.tmem;
   const int n_tiles = (int)(sh.tiles_before[1] - sh.tiles_before[0]);
 
   // warp-uniform bounded wait, kept short (it stands in many places); a role that gives up ends, and with
@@ -871,6 +941,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
     } else if (warp < W_ACC) {
       // ---- softmax: one token a thread, rows col0 .. col0 + NH - 1 ----
       qb_registers<qb_shares(N).softmax, true>();
+      pdl_wait();
       const int group = (warp - 8) >> 2, q4 = warp & 3, col0 = group * NH;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       const int tok = 32 * q4 + lane;
@@ -1054,6 +1125,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
     } else if (warp < W_COPY) {
       // ---- accumulation: one channel a thread ----
       qb_registers<qb_shares(N).acc, true>();
+      pdl_wait();
       const int q4 = warp & 3, wt = tid - 32 * W_ACC;
       const uint32_t lanes = (uint32_t)(32 * q4) << 16;
       constexpr int TPR = 128 / N;  // threads a query row
@@ -1063,6 +1135,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       QbUnit u{};
       int i = 0;
       bool done = false;
+      int4 join = make_int4(0, 0, 0, 0);
       arrive(&sh.p_ready[0]);  // nothing to read before tiles 0 and 1
       arrive(&sh.p_ready[1]);
       // round un: the queries of unit un + 1 into their buffer, then unit un
@@ -1161,6 +1234,12 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           for (int j = 0; j < N; ++j) s_out[j * D + wt] = acc[j];
           if (!wait(&sh.lz_ready, un)) break;
           const bool whole = u.t0 == 0 && u.t1 == u.nt;
+          if (u.t0 == 0 && !whole) {  // the following slices hold the other nt - t1 tiles
+            const QbSlices slices(sh.work, gridDim.x);
+            int parts = 1;
+            while (slices.start(blockIdx.x + 1 + parts) - slices.start(blockIdx.x + 1) < u.nt - u.t1) ++parts;
+            join = make_int4(u.c0, u.n, u.rt * a.g.n_kv_heads + u.h, 1 + parts);
+          }
           float* part_out = a.ws.part + (size_t)(2 * blockIdx.x + (u.t0 == 0 ? 1 : 0)) * N * (D + 2);
           if (wt < N) {
             const float l = (sh.lsum[0][wt] + sh.lsum[1][wt]) + (sh.lsum[2][wt] + sh.lsum[3][wt]);
@@ -1193,6 +1272,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         u = next;
       }
       if (!done) gave_up();
+      if (wt == 0) a.ws.join[blockIdx.x] = join;
     } else if (warp == W_COPY) {
       qb_registers<qb_shares(N).misc, false>();
       // ---- page copies, and the list of units one ahead of them ----
@@ -1300,6 +1380,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
       }
     }
   }
+  if (n_tiles == 0 && tid == 0) a.ws.join[blockIdx.x] = make_int4(0, 0, 0, 0);
+  pdl_wait();  // also of a CTA without tiles: what follows this grid follows the preparation
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -1313,31 +1395,16 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
 constexpr int QB_JOIN_ROWS = 8;  // a warp a row
 
 template <int N>
-__global__ void __launch_bounds__(32 * QB_JOIN_ROWS) qb_combine_kernel(QbArgs a, int grid) {
-  const int lane = threadIdx.x & 31, r = blockIdx.y * QB_JOIN_ROWS + (threadIdx.x >> 5);
-  // the list of work is complete: the attention's blocks waited for it before they let this grid start
-  const QbSlices slices(a.ws.work[a.n_seqs], grid);
-  const int k = blockIdx.x;
-  const long long start = slices.start(k), end = slices.start(k + 1);
-  if (end == start) {
-    pdl_wait();  // every block ends after the attention, so that what follows this grid does too
-    return;
-  }
-  int in;
-  long long before;
-  const QbUnit u = qb_locate<N>(a, end - 1, lane, in, before);
-  const long long u0 = end - 1 - in + QB_UNIT_WORK, u1 = u0 + u.nt;  // the work of its tiles
-  const int R = u.rt * N + r, tk = R >> a.gqa_shift;
-  if (u1 <= end || u0 < start || u0 >= end || tk >= u.n) {
-    pdl_wait();
-    return;
-  }
-  int parts = 1;  // slices after k are not empty before u1: sizes differ by one, larger ones first
-  while (slices.start(k + parts) < u1) ++parts;
+__global__ void __launch_bounds__(32 * QB_JOIN_ROWS) qb_combine_kernel(QbArgs a) {
+  const int lane = threadIdx.x & 31, r = blockIdx.y * QB_JOIN_ROWS + (threadIdx.x >> 5), k = blockIdx.x;
+  pdl_wait();
+  const int4 join = a.ws.join[k];
+  const int parts = join.w, rt = join.z / a.g.n_kv_heads, h = join.z % a.g.n_kv_heads;
+  const int R = rt * N + r, tk = R >> a.gqa_shift;
+  if (parts == 0 || tk >= join.y) return;
   const float* first = a.ws.part + (size_t)(2 * k + 1) * N * (D + 2);
   const float* rest = a.ws.part + (size_t)(2 * k) * N * (D + 2);  // + 2 j slots: slice k + j
   const size_t step = (size_t)2 * N * (D + 2);
-  pdl_wait();
   // the largest reference, of parts with visible tokens (l != 0)
   float m = -INFINITY;
   for (int j = lane; j < parts; j += 32) {
@@ -1356,7 +1423,7 @@ __global__ void __launch_bounds__(32 * QB_JOIN_ROWS) qb_combine_kernel(QbArgs a,
     l = fmaf(pl, f, l);
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  *reinterpret_cast<float4*>(a.out + ((size_t)(u.c0 + tk) * a.n_q_heads + u.h * a.gqa + (R & (a.gqa - 1))) * D + 4 * lane) =
+  *reinterpret_cast<float4*>(a.out + ((size_t)(join.x + tk) * a.n_q_heads + h * a.gqa + (R & (a.gqa - 1))) * D + 4 * lane) =
       make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
@@ -1395,7 +1462,7 @@ static cudaError_t qb_launch(const QbArgs& a, const int32_t* parents, const void
   qb_prepare_kernel<N><<<(unsigned)blocks, QB_PREP_THREADS, 0, s>>>(a, parents, q, dtype, rot, chunks);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = qb_launch_pdl(qb_attend_kernel<N>, dim3(grid), QB_THREADS, qb_smem_bytes(N), s, a)) != cudaSuccess) return e;
-  return qb_launch_pdl(qb_combine_kernel<N>, dim3(grid, N / QB_JOIN_ROWS), 32 * QB_JOIN_ROWS, 0, s, a, grid);
+  return qb_launch_pdl(qb_combine_kernel<N>, dim3(grid, N / QB_JOIN_ROWS), 32 * QB_JOIN_ROWS, 0, s, a);
 }
 
 cudaError_t launch_query_block(const PageGeom& g, int n_q_heads, int n_seqs, int n_total, const void* q, int dtype,
