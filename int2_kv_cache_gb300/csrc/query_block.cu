@@ -1405,22 +1405,35 @@ __global__ void __launch_bounds__(32 * QB_JOIN_ROWS) qb_combine_kernel(QbArgs a)
   const float* first = a.ws.part + (size_t)(2 * k + 1) * N * (D + 2);
   const float* rest = a.ws.part + (size_t)(2 * k) * N * (D + 2);  // + 2 j slots: slice k + j
   const size_t step = (size_t)2 * N * (D + 2);
-  // the largest reference, of parts with visible tokens (l != 0)
-  float m = -INFINITY;
-  for (int j = lane; j < parts; j += 32) {
-    const float* p = (j ? rest + j * step : first) + N * D;
-    m = fmaxf(m, p[r] != 0.f ? p[N + r] : -INFINITY);
-  }
-  m = warp_max(m);
+  // eight parts at a time, their loads in flight together, into a running sum (a part without visible tokens, l = 0, has
+  // no reference)
+  float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 8
-  for (int j = 0; j < parts; ++j) {
-    const float* p = j ? rest + j * step : first;
-    const float pl = p[N * D + r], f = pl != 0.f ? exp2f(p[N * D + N + r] - m) : 0.f;
-    const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * lane);
-    o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
-    l = fmaf(pl, f, l);
+  for (int j0 = 0; j0 < parts; j0 += 8) {
+    float pm[8], pl[8];
+    float4 v[8];
+    float top = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = j0 + j < parts;
+      const float* p = j0 + j ? rest + (in ? j0 + j : 1) * step : first;
+      pl[j] = in ? p[N * D + r] : 0.f;
+      pm[j] = p[N * D + N + r];
+      v[j] = *reinterpret_cast<const float4*>(p + r * D + 4 * lane);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, pl[j] != 0.f ? pm[j] : -INFINITY);
+    const float f0 = l != 0.f ? exp2f(m - top) : 0.f;
+    m = top;
+    l *= f0;
+    o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (pl[j] == 0.f) continue;
+      const float f = exp2f(pm[j] - m);
+      o.x = fmaf(v[j].x, f, o.x); o.y = fmaf(v[j].y, f, o.y); o.z = fmaf(v[j].z, f, o.z); o.w = fmaf(v[j].w, f, o.w);
+      l = fmaf(pl[j], f, l);
+    }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
   *reinterpret_cast<float4*>(a.out + ((size_t)(join.x + tk) * a.n_q_heads + h * a.gqa + (R & (a.gqa - 1))) * D + 4 * lane) =
