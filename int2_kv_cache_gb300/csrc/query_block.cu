@@ -753,16 +753,25 @@ template <int N>
 __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
   constexpr int NG = QB_GROUPS, NH = N / NG;  // groups of softmax warps, rows of a group
   constexpr int W_ACC = 8 + 4 * NG, W_COPY = W_ACC + 4, W_MMA = W_COPY + 1;  // first warps of the roles
+  // Up to 32 rows the two halves of an fp32 operand stand side by side as 2 N columns of one product, whose two results are
+  // added by the reader: an MMA of few columns takes as long as its A operand (about 35 cycles), so half as many MMAs
+  // run in half the time.  64 rows: one product after the other into the same columns.
+  constexpr bool PAIR = N <= 32;
   constexpr uint32_t T_K = 0, T_V = 128, T_S = 256, T_O = 384;  // tensor memory columns, two buffers of 64 each
   extern __shared__ uint8_t qb_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(qb_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* s_q = smem;                          // [2 units][hi, lo][2 halves of 64 channels][N rows of 128 bytes]
-  uint8_t* s_p = s_q + 2 * N * 512;             // [2 tiles][hi, lo][128 tokens of 128 bytes]
+  uint8_t* s_q = smem;                          // [2 units][hi, lo][2 halves of 64 channels][N rows of 128 bytes]; PAIR: [units][halves][hi, lo][N]
+  uint8_t* s_p = s_q + 2 * N * 512;             // [2 tiles][hi, lo][128 tokens of 128 bytes]; PAIR: [tiles][1][tokens of N hi, N lo]
   uint8_t* s_stage = s_p + 4 * QB_PBUF;
   float* s_out = reinterpret_cast<float*>(s_stage + QB_STAGES * QB_STAGE_BYTES);  // [N][128] of a finished unit
   __shared__ QbShared<N> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr unsigned FULLM = 0xffffffffu;
+  constexpr int Q_LO = PAIR ? N * 128 : N * 256, Q_HALF = PAIR ? 2 * N * 128 : N * 128;  // bytes from hi to lo, from half to half
+  // byte of the 16-byte chunk `c` (8 rows) of a token's hi (0) or lo (1) weights
+  auto p_at = [](int part, int c, int token) {
+    return PAIR ? token * 128 + (((c + part * (N / 8)) ^ (token & 7)) << 4) : part * QB_PBUF + token * 128 + ((c ^ (token & 7)) << 4);
+  };
 
   // Up to QB_FEW sequences the list of work, the pages and their expansion need nothing of the preparation: only the
   // warps that read its queries and trees wait for it.
@@ -1008,12 +1017,18 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
                       inv = tc[QB_C_INV][tok], zc = tc[QB_C_ZC][tok];
           const uint64_t sk2 = f2pk(sk, sk), kmid2 = f2pk(kmid, kmid), ls2 = f2pk(ls, ls), inv2 = f2pk(inv, inv),
                          zc2 = f2pk(zc, zc);
-          uint8_t* p_hi = s_p + (2 * buf) * QB_PBUF + tok * 128;
+          uint8_t* weights = s_p + (2 * buf) * QB_PBUF;
           const uint32_t scores = tmem + lanes + T_S + 64 * buf + col0;
           if (lead) sh.moved[i & 3][group] = 0;
           // x: a + log2 s - M, -infinity where the row does not see the token
           float x[NH], top = -INFINITY;
           qb_tmem_ld<NH>(scores, x);
+          if constexpr (PAIR) {
+            float y[NH];
+            qb_tmem_ld<NH>(scores + N, y);
+#pragma unroll
+            for (int j = 0; j < NH; ++j) x[j] += y[j];
+          }
 #pragma unroll
           for (int j = 0; j < NH; j += 4) {
             const float4 sq = *reinterpret_cast<const float4*>(s_sumq + col0 + j);
@@ -1078,9 +1093,9 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
               const float2 r = f2up(f2sub(f2pk(w0, w1), f2pk(back.x, back.y)));
               lo[k] = qb_half2(r.x, r.y);
             }
-            const int at = (((col0 + j) >> 3) ^ (tok & 7)) << 4;
-            *reinterpret_cast<uint4*>(p_hi + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(p_hi + QB_PBUF + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            const int c = (col0 + j) >> 3;
+            *reinterpret_cast<uint4*>(weights + p_at(0, c, tok)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(weights + p_at(1, c, tok)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
           tc_fence_before();
           fence_proxy_async();
@@ -1098,9 +1113,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
         if ((i > 0 && !(ok = wait(&sh.o_done[(i - 1) & 1], (i - 1) >> 1))) || (un && !(ok = wait(&sh.lz_free, un - 1))))
           continue;
         uint8_t* mine = s_p + 2 * ((i + 1) & 1) * QB_PBUF;
-        auto at = [&](int row, int token) {  // two 8-row chunks' places (hi and lo) hold 8 rows of fp32
-          return mine + ((row >> 2) & 1) * QB_PBUF + token * 128 + ((((col0 + row) >> 3) ^ (token & 7)) << 4);
-        };
+        // a chunk's two places (hi and lo) hold 8 rows of fp32
+        auto at = [&](int row, int token) { return mine + p_at((row >> 2) & 1, (col0 + row) >> 3, token); };
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
@@ -1185,12 +1199,12 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
               lo[f] = qb_half2(x - back.x, y - back.y);
             }
             const int w = (part * N + j) >> 4;  // 16-channel word
-            uint8_t* d = dst + (w >> 2) * N * 128;
+            uint8_t* d = dst + (w >> 2) * Q_HALF;
             const int c0 = ((2 * (w & 3)) ^ (row & 7)) << 4, c1 = ((2 * (w & 3) + 1) ^ (row & 7)) << 4;
             *reinterpret_cast<uint4*>(d + c0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(d + c1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-            *reinterpret_cast<uint4*>(d + N * 256 + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            *reinterpret_cast<uint4*>(d + N * 256 + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+            *reinterpret_cast<uint4*>(d + Q_LO + c0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(d + Q_LO + c1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
           }
           if (part == 0) {
             sh.sumq[buf][row] = s;
@@ -1215,6 +1229,12 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             for (int c = 0; c < NG; ++c) {
               float o[NH];
               qb_tmem_ld<NH>(tmem + lanes + T_O + 64 * buf + c * NH, o);
+              if constexpr (PAIR) {
+                float low[NH];
+                qb_tmem_ld<NH>(tmem + lanes + T_O + 64 * buf + N + c * NH, low);
+#pragma unroll
+                for (int j = 0; j < NH; ++j) o[j] += low[j];
+              }
               if (sh.moved[i & 3][c]) {
 #pragma unroll
                 for (int j = 0; j < NH; ++j) acc[c * NH + j] *= sh.scale[i & 3][c * NH + j];
@@ -1328,7 +1348,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
     } else {
       qb_registers<qb_shares(N).misc, false>();
       // ---- MMA issue ----
-      constexpr uint32_t I_QK = qb_idesc(N, false), I_PV = qb_idesc(N, true);
+      constexpr int COLS = PAIR ? 2 * N : N, PARTS = PAIR ? 1 : 2;
+      constexpr uint32_t I_QK = qb_idesc(COLS, false), I_PV = qb_idesc(COLS, true);
       int un = -1, left = 0;
       uint64_t q = 0;
       bool ok = true;
@@ -1348,10 +1369,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           if (qb_elect()) {
             const uint32_t ak = tmem + T_K + 64 * buf, d = tmem + T_S + 64 * buf;
 #pragma unroll 1
-            for (int p = 0; p < 2; ++p)  // lo, then hi: 4 steps of 16 channels in each of two halves
+            for (int p = 0; p < PARTS; ++p)  // (lo, then hi:) 4 steps of 16 channels in each of two halves
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                tc_mma_f16_ts(d, ak + 8 * k, q + ((p ? 0 : 2) + (k >> 2)) * (N * 128 >> 4) + (k & 3) * 2, I_QK, p + k > 0);
+                tc_mma_f16_ts(d, ak + 8 * k, q + ((PAIR || p ? 0 : Q_LO) + (k >> 2) * Q_HALF) / 16 + (k & 3) * 2, I_QK, p + k > 0);
             tc_commit(&sh.s_done[buf]);
           }
           __syncwarp();
@@ -1364,9 +1385,10 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             const uint64_t hi = sw128_desc(s_p + (2 * buf) * QB_PBUF), lo = sw128_desc(s_p + (2 * buf + 1) * QB_PBUF);
             const uint32_t av = tmem + T_V + 64 * buf, d = tmem + T_O + 64 * buf;
 #pragma unroll 1
-            for (int p = 0; p < 2; ++p)
+            for (int p = 0; p < PARTS; ++p)
 #pragma unroll
-              for (int k = 0; k < 8; ++k) tc_mma_f16_ts(d, av + 8 * k, (p ? hi : lo) + k * (2048 >> 4), I_PV, p + k > 0);
+              for (int k = 0; k < 8; ++k)
+                tc_mma_f16_ts(d, av + 8 * k, (PAIR || p ? hi : lo) + k * (2048 >> 4), I_PV, p + k > 0);
             tc_commit(&sh.o_done[buf]);
           }
           __syncwarp();
