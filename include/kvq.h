@@ -348,7 +348,7 @@ kvq_status kvq_query_block_workspace_size(const kvq_layout* layout, int n_seqs, 
  *   workspace: >= kvq_query_block_workspace_size bytes, 16-byte aligned; one call at a time may use it
  * Results do not depend on timing.  Sequences with inconsistent lengths and out-of-range block ids are flagged
  * (kvq_device_check) and their outputs are unspecified; a bad parent is flagged and taken as -1.
- * n_seqs <= 65535; query heads per KV head 1, 2, 4 or 8. */
+ * n_seqs <= 65535; max_seq_len <= 2^31 - 257; query heads per KV head 1, 2, 4 or 8. */
 kvq_status kvq_tree_attention(const kvq_layout* layout, int n_seqs, int n_q_total, const void* q, kvq_dtype q_dtype,
                               const int32_t* cu_q, int max_q, const int32_t* parents, const int32_t* seq_lens,
                               int max_seq_len, const int32_t* block_table, kvq_rot rot_k, const uint8_t* pool,

@@ -681,6 +681,7 @@ static kvq_status check_query_block(const kvq_layout* layout, int n_seqs, int n_
                 max_seq_len);
   if ((long long)n_q_total * layout->n_q_heads >= (1ll << 31))
     return fail(KVQ_EUNSUPPORTED, "n_q_total * n_q_heads >= 2^31");
+  if (max_seq_len > INT32_MAX - 256) return fail(KVQ_EUNSUPPORTED, "max_seq_len %d > 2^31 - 257", max_seq_len);
   return check_decode_size(layout, n_seqs, max_seq_len);
 }
 

@@ -144,6 +144,8 @@ TREES = [
     (32, 8, 16, [2049], [31], "signed_hadamard", "bf16", random_tree),
     (3, 3, 8, [70, 641, 9], [64, 1, 0], "identity", "bf16", random_tree),
     (4, 2, 16, [400], [300], "dense", "bf16", random_tree),           # a tree over several row tiles and key tiles
+    (2, 1, 8, [300], [300], "identity", "f32", star),                 # slices in which a row sees nothing
+    (1, 1, 16, [1030], [1024], "signed_hadamard", "bf16", random_tree),  # the largest tree
 ]
 
 
@@ -182,6 +184,27 @@ def test_cross(hq, hkv, page, lens, ns, rot, dtype):
     blk.check(blk.run(cross=True), cross=True)
 
 
+@pytest.mark.parametrize("n", [127, 128, 129, 300])
+@pytest.mark.parametrize("cross", [False, True])
+def test_many_short_sequences(n, cross):
+    """Around the number of sequences up to which every block lists the work itself; several units a slice."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 40, n).tolist()
+    ns = [int(rng.integers(0, 12)) if cross else int(rng.integers(0, min(12, x) + 1)) for x in lens]
+    blk = Block(20, 8, 4, 8, lens, ns, "dense", "bf16")
+    blk.check(blk.run(cross), cross=cross, seqs=range(0, n, 5))
+
+
+@pytest.mark.parametrize("hq,n", [(2, 5), (8, 3), (8, 30)])  # 10, 24 and 240 rows: each size of row tile
+def test_logits_that_keep_rising(hq, n):
+    """Keys that grow along the sequence, so that the running maximum passes every reference again and again."""
+    blk = Block(21, hq, 1, 16, [2100], [n], "dense", "f32", random_tree, q_scale=3.0)
+    for pos in range(2100):
+        s = 0.02 * 1.0035 ** pos
+        set_meta(blk.pool, 16, 0, blk.table[0, pos // 16], pos % 16, s, -1.5 * s)
+    blk.check(blk.run())
+
+
 def test_many_sequences_and_long_contexts():
     rng = np.random.default_rng(9)
     lens = rng.integers(1, 90, 200).tolist() + [20011]
@@ -191,8 +214,9 @@ def test_many_sequences_and_long_contexts():
 
 
 @pytest.mark.parametrize("q_scale", [1e-3, 30.0])
-def test_flat_and_peaked_softmax(q_scale):
-    blk = Block(5, 8, 2, 16, [3001, 260], [9, 20], "dense", "f32", random_tree, q_scale=q_scale)
+@pytest.mark.parametrize("ns", [[9, 20], [2, 4], [5, 8]])
+def test_flat_and_peaked_softmax(q_scale, ns):
+    blk = Block(5, 8, 2, 16, [3001, 260], ns, "dense", "f32", random_tree, q_scale=q_scale)
     blk.check(blk.run())
 
 

@@ -51,6 +51,9 @@ def test_query_block_rejects_bad_arguments(kvq, name):
     assert _tree(kvq, lay, name, n_seqs=65536) == kvq.KVQ_EUNSUPPORTED
     assert _tree(kvq, lay, name, total=(1 << 31) - 1) == kvq.KVQ_EUNSUPPORTED
     assert _tree(kvq, _layout(kvq, n_q_heads=24), name) == kvq.KVQ_EUNSUPPORTED
+    long = _layout(kvq, n_kv_heads=1, n_q_heads=1, max_blocks_per_seq=(1 << 27) - 1)
+    assert _tree(kvq, long, name, n_seqs=1, max_len=(1 << 31) - 16) == kvq.KVQ_EUNSUPPORTED
+    assert "2^31" in err()
     bad = _layout(kvq)
     bad.head_dim = 64
     assert _tree(kvq, bad, name) == kvq.KVQ_EUNSUPPORTED
