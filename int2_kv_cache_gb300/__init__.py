@@ -29,7 +29,13 @@ With BF16 sink / recent windows, add ``win = kvq.Window(64, 256, buf)`` (``buf``
 ``kvq.Window.buffer_bytes(n_seqs, 8, 64, 256)`` bytes), call ``kvq_window_append(lay,
 k, v, cu_new, start_pos, mu, win)`` beside the append, and decode with
 ``kvq_decode_attention_win(lay, q, seq_lens, max_len, table, rk, rv, pool, win, ws, o_rot)``
-(workspace from ``kvq_decode_workspace_size_win``).  Candidate selection:
+(workspace from ``kvq_decode_workspace_size_win``).
+
+Speculative decoding on the same pool: ``kvq_plan_pages`` (old -> new lengths: pages, ``cu_new``, slots),
+``kvq_quantize_append`` (the drafts), ``kvq_tree_attention(lay, q, cu_new, max_drafts, parents, lens, max_len, table,
+rk, pool, ws, o_rot)`` (workspace from ``kvq_query_block_workspace_size``), ``kvq_tree_commit`` (the accepted path) and
+``kvq_plan_pages`` again for the pages of the rejected drafts.  ``kvq_cross_attention``: query blocks over an encoder's
+cached states.  Candidate selection:
 ``kvq_calib_nmse``; per-head error report: ``kvq_head_error_report``.
 """
 from __future__ import annotations
