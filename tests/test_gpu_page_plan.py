@@ -244,3 +244,55 @@ def test_speculative_step_equals_decoding_one_token_at_a_time(rot, dtype, page):
             for x, y in zip(gu.seq_codes_meta(pool.cpu().numpy(), hkv, page, table[b].cpu().numpy(), length, which),
                             gu.seq_codes_meta(alone.cpu().numpy(), hkv, page, own_table[b].cpu().numpy(), length, which)):
                 assert np.array_equal(x, y)
+
+
+@pytest.mark.parametrize("n", [4, 1100])  # both sizes of the plan's blocks
+def test_a_captured_grow_commit_shrink_step_replays(n):
+    """One graph: grow by the drafts, commit, give pages back, with the ring's counters going from one pair to the other
+    and back; replayed with new drafts and paths, it follows the oracle."""
+    import oracle
+    page, mb, h, most = 8, 12, 2, 6
+    p = Pages(31, n, page, mb, mb * n)
+    kvq, t, rng, blocks = p.kvq, p.torch, p.rng, p.blocks
+    lay = kvq.make_layout(page, h, h, blocks, mb)
+    pool = rng.integers(0, 256, blocks * h * 72 * page, dtype=np.uint8)
+    d_pool, table, ring = t.from_numpy(pool.copy()).cuda(), gu.dev_i32(p.table), gu.dev_i32(p.ring)
+    pairs = [t.tensor([p.head, p.tail], device="cuda"), t.zeros(2, dtype=t.int64, device="cuda")]
+    lens, grown, kept = (t.zeros(n, dtype=t.int32, device="cuda") for _ in range(3))
+    acc, n_acc = t.zeros(n, most, dtype=t.int32, device="cuda"), t.zeros(n, dtype=t.int32, device="cuda")
+    cu, cu2 = (t.zeros(n + 1, dtype=t.int32, device="cuda") for _ in range(2))
+    slots, none = t.zeros(most * n, dtype=t.int64, device="cuda"), t.zeros(0, dtype=t.int64, device="cuda")
+    ws = t.empty(kvq.kvq_plan_workspace_size(n), dtype=t.uint8, device="cuda")
+
+    def step():
+        kvq.kvq_plan_pages(lay, lens, grown, table, ring, pairs[0], pairs[1], cu, slots, ws)
+        kvq.kvq_tree_commit(lay, cu, acc, n_acc, slots, grown, kept, d_pool)
+        kvq.kvq_plan_pages(lay, grown, kept, table, ring, pairs[1], pairs[0], cu2, none, ws)
+        lens.copy_(kept)
+
+    step()  # nothing grows: changes nothing
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        step()
+    at = np.zeros(n, np.int64)
+    for _ in range(5):
+        drafts = rng.integers(0, most + 1, n)
+        count = np.array([rng.integers(0, x + 1) for x in drafts])
+        paths = np.zeros((n, most), np.int64)
+        for b in range(n):
+            paths[b, :count[b]] = np.sort(rng.permutation(drafts[b])[:count[b]])
+        grown.copy_(gu.dev_i32(at + drafts))
+        acc.copy_(gu.dev_i32(paths))
+        n_acc.copy_(gu.dev_i32(count))
+        graph.replay()
+        kvq.kvq_device_check()
+        p.table, p.ring, p.head, p.tail, c, s = oracle.tree.plan_pages(
+            page, blocks, at, at + drafts, p.table, p.ring, p.head, p.tail, most * n)
+        pool, new = oracle.tree.commit(pool, h, page, c, paths, count, s, at + drafts)
+        p.table, p.ring, p.head, p.tail = oracle.tree.plan_pages(
+            page, blocks, at + drafts, new, p.table, p.ring, p.head, p.tail, 0)[:4]
+        at = np.asarray(new, np.int64)
+        for name, g, w in (("table", table, p.table), ("ring", ring, p.ring), ("counters", pairs[0], [p.head, p.tail]),
+                           ("lens", lens, at), ("slots", slots, s), ("pool", d_pool, pool)):
+            np.testing.assert_array_equal(g.cpu().numpy(), w, err_msg=name)

@@ -372,3 +372,20 @@ def test_bad_parents_are_flagged_and_taken_as_roots():
     got = _flagged(blk, d)
     blk.parents = np.array([-1, 0, -1, 1, -1, 4], np.int32)
     blk.check(got)
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    blocks = [Block(41, 8, 2, 16, [3000, 700], [13, 40], "dense", "bf16", random_tree),
+              Block(42, 2, 1, 8, [2500, 90, 33], [5, 2, 1], "signed_hadamard", "f32", random_tree)]
+    want = [b.run() for b in blocks]
+    ds = [b.device() for b in blocks]
+    torch = blocks[0].torch
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for b, d, s in zip(blocks, ds, streams):
+            b.launch(d, stream=s)
+    torch.cuda.synchronize()
+    blocks[0].kvq.kvq_device_check()
+    for w, d in zip(want, ds):
+        assert np.array_equal(w, d["o"].cpu().numpy())
