@@ -70,6 +70,7 @@ constexpr int QB_UNIT_WORK = 3;                   // what starting and ending a 
 // the same at 2^6), and again whenever a weight would pass 2^15.5.
 constexpr float QB_LIFT = 3.f, QB_TRIGGER = 15.5f;
 
+constexpr int QB_APART = INT32_MIN;               // a unit's limit of open positions where its rows are far apart in size
 constexpr int QB_GROUPS = 2;                      // groups of four softmax warps, half of the rows each
 // Keys (4 warps), values (4), softmax, accumulation (4), copies, MMA issue and two idle warps: register shares go by four.
 constexpr int QB_THREADS = 32 * (16 + 4 * QB_GROUPS);
@@ -615,6 +616,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       QB_R8(r, 0), QB_R8(r, 8)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&v)[8]) {
+  uint32_t r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(v[i]);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), QB_R8(r, 0)
+               : "memory");
+}
 // 16 lanes x 16 columns: thread t holds row t / 4 (and + 8), column t % 4 of every group of four columns
 __device__ __forceinline__ void tmem_st16x128_x4(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), QB_R8(r, 0)
@@ -740,7 +748,9 @@ struct QbShared {  // alignas: read as 16-byte vectors
   alignas(8) long long tiles_before[2];  // the slice's two ends
   long long work;                        // of all slices
   float unscale[2];                 // what the products of key codes and queries are scaled back by
-  float qmax[2][4];
+  bool apart[2];                    // rows far apart in size: unscale is 1, and each row has its own row_unscale
+  alignas(16) float row_unscale[2][N];
+  uint32_t qmax[2][4], qmin[2][4];  // bits of the warps' largest and smallest row maxima (of rows that are not all zero)
   float row_z[N], row_f[N];         // of the unit being written out
   alignas(8) uint64_t full[QB_STAGES];
   uint64_t empty[QB_STAGES];
@@ -986,8 +996,9 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             len = u.len;
             c0 = u.c0;
             base = a.mode == QB_CROSS ? u.len : u.len - u.n;
-            // positions below `open` are seen by every row of the tile
-            open = a.mode == QB_CHAIN ? base + u.rt * (N >> a.gqa_shift) + 1 : base;
+            // positions below `open` are seen by every row of the tile (a unit with rows far apart in size: none, so that
+            // every tile goes through the branch where their scores are scaled back)
+            open = sh.apart[un & 1] ? QB_APART : a.mode == QB_CHAIN ? base + u.rt * (N >> a.gqa_shift) + 1 : base;
             arrive(&sh.unit_free[un % QB_UNITS]);
             unscale = sh.unscale[un & 1];
             s_sumq = sh.sumq[un & 1];
@@ -1004,6 +1015,22 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
           int key_tin = 0;
           unsigned key_size = 0x7fffffffu;
           if (__builtin_expect(masked && ok, 0)) {
+            if (open == QB_APART && (ok = wait(&sh.s_done[buf], use))) {
+              tc_fence_after();
+              const float* back = sh.row_unscale[un & 1] + col0;
+#pragma unroll 1
+              for (int j = 0; j < NH; j += 8)
+#pragma unroll 1
+                for (int part = 0; part < (PAIR ? 2 : 1); ++part) {
+                  float v[8];
+                  const uint32_t at = tmem + lanes + T_S + 64 * buf + part * N + col0 + j;
+                  tmem_ld8(at, v);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) v[k] *= back[j + k];
+                  tmem_st8(at, v);
+                }
+              tmem_wait_st();
+            }
             const int d = t * QB_TOK + tok - base;
             if (d + base >= len) {
               key_size = 0u;
@@ -1187,14 +1214,30 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             m = w <= 3.0e38f ? fmaxf(m, w) : m;  // of the finite ones
           }
 #pragma unroll
-          for (int d = 1; d < TPR; d <<= 1) s += __shfl_xor_sync(FULLM, s, d);
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(FULLM, m, d));
-          if (lane == 0) sh.qmax[buf][q4] = m;
+          for (int d = 1; d < TPR; d <<= 1) {
+            s += __shfl_xor_sync(FULLM, s, d);
+            m = fmaxf(m, __shfl_xor_sync(FULLM, m, d));  // the row's
+          }
+          // non-negative floats are in the order of their bits
+          uint32_t top = __reduce_max_sync(FULLM, __float_as_uint(m));
+          uint32_t low = __reduce_min_sync(FULLM, m > 0.f ? __float_as_uint(m) : 0x7f7fffffu);
+          if (lane == 0) {
+            sh.qmax[buf][q4] = top;
+            sh.qmin[buf][q4] = low;
+          }
           if (!meet()) break;
-          m = fmaxf(fmaxf(sh.qmax[buf][0], sh.qmax[buf][1]), fmaxf(sh.qmax[buf][2], sh.qmax[buf][3]));
-          // the largest at 2^13 .. 2^14
-          const int e = m > 0.f ? min(100, max(-100, 13 - ((int)(__float_as_uint(m) >> 23) - 127))) : 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            top = max(top, sh.qmax[buf][k]);
+            low = min(low, sh.qmin[buf][k]);
+          }
+          // One power of two for the tile puts its largest row at 2^13 .. 2^14.  fp16's step is 2^-24 at least, so a row keeps
+          // the 22 bits of its two halves down to 2^-16 of the largest.  Where some row is smaller, each has a power of its
+          // own, and its scores are scaled back by it, so that no row's precision depends on another's size (multiplied into
+          // every score of every tile, the rows' own powers cost 11 % of a long call: 357 -> 395 us on 16 trees of 32 drafts on 16k).
+          const bool apart = (int)(top >> 23) - (int)(low >> 23) > 16;
+          const uint32_t of = apart ? __float_as_uint(m) : top;
+          const int e = of ? min(100, max(-100, 13 - ((int)(of >> 23) - 127))) : 0;
           const float scale = __uint_as_float((uint32_t)(127 + e) << 23);
           uint8_t* dst = s_q + buf * N * 512 + row * 128;
 #pragma unroll
@@ -1222,7 +1265,12 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             sh.tin[buf][row] =
                 !valid ? 0 : a.mode == QB_TREE ? a.ws.tree[next.c0 + tk].x : a.mode == QB_CHAIN ? tk : 0;
           }
-          if (wt == 0) sh.unscale[buf] = __uint_as_float((uint32_t)(127 - e) << 23);
+          const float back = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (part == 0) sh.row_unscale[buf][row] = back;
+          if (wt == 0) {
+            sh.unscale[buf] = apart ? 1.f : back;
+            sh.apart[buf] = apart;
+          }
           fence_proxy_async();
           arrive(&sh.q_ready[buf]);
         }
