@@ -59,6 +59,26 @@ def test_tiny_rows_beside_normal_ones():
     blk.check(blk.run())
 
 
+@pytest.mark.parametrize("size", [2e34, 1e36, 2e37])
+def test_a_tile_of_huge_rows_is_finite(size):
+    """Rows whose logits are within fp32: a softmax of one token, however large (the scores' own rounding decides ties
+    of such logits, so the key that wins is far ahead of the others)."""
+    blk = Block(54, 2, 1, 16, [40], [4], "identity", "f32")
+    blk.q[:] = np.float32(size)
+    pos = 17
+    for p in range(40):
+        s, z = (0.0, 0.5) if p == pos else (0.0, -0.25)
+        at = (p // 16, p % 16)
+        rec = blk.pool[blk.table[0, at[0]], 0]
+        rec[32 * at[1]:32 * at[1] + 32] = 0
+        rec[64 * 16 + 4 * at[1]:64 * 16 + 4 * at[1] + 4] = np.array([s, z], np.float16).view(np.uint8)
+    got = blk.run()
+    import oracle
+    _, vh = oracle.cache.dequantized_sequence(blk.pool.reshape(-1), 1, 16, blk.table[0], 40)
+    want = np.broadcast_to(vh[pos, 0], got.shape)
+    np.testing.assert_allclose(got, want, rtol=0, atol=2.0 ** -18 * np.abs(vh[pos]).max())
+
+
 @pytest.mark.parametrize("hq,n", [(1, 9), (8, 8)])
 def test_rows_of_very_different_size_over_many_units(hq, n):
     """Units with and without rows far apart follow one another in the same buffers."""
