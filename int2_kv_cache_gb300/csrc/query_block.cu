@@ -69,6 +69,11 @@ constexpr int QB_UNIT_WORK = 3;                   // what starting and ending a 
 // Weights: the running maximum is put at 2^3 (further from fp16's smallest step than at 1: readout error 6.5e-7 -> 4.6e-7,
 // the same at 2^6), and again whenever a weight would pass 2^15.5.
 constexpr float QB_LIFT = 3.f, QB_TRIGGER = 15.5f;
+// A weight's second half is held times 2^11: up to half a step of the largest weight (2^15), and down to 2^-36 in all.
+// Unscaled, weights ended at fp16's 2^-25, 2^-28 of the largest: behind a token 19 nats above 131,071 others, a third of
+// a per mille of the readout was lost.
+constexpr int QB_LO_SHIFT = 11;
+constexpr float QB_LO_UP = 2048.f, QB_LO_DOWN = 1.f / 2048.f;
 
 constexpr int QB_APART = INT32_MIN;               // a unit's limit of open positions where its rows are far apart in size
 constexpr int QB_GROUPS = 2;                      // groups of four softmax warps, half of the rows each
@@ -587,13 +592,21 @@ qb_prepare_kernel(QbArgs a, const int32_t* __restrict__ parents, const void* __r
 // ---------------------------------------------------------------------------
 // Tensor memory wrappers of this kernel
 // ---------------------------------------------------------------------------
-// D[tmem] (+)= A[tmem] B[smem]^T, fp16 operands, by one thread.
+// D[tmem] (+)= A[tmem] B[smem]^T, fp16 operands, by one thread; D enters times 2^-SHIFT.
+template <int SHIFT = 0>
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)acc)
-      : "memory");
+  if constexpr (SHIFT == 0)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, %5;\n}" ::"r"(d),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)acc), "n"(SHIFT)
+        : "memory");
 }
 // One lane of a converged warp, in the form from which the compiler knows that the code
 // under it runs in a single thread (its matrix operands then need no per-lane loop).
@@ -1127,7 +1140,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
               const float w0 = x[j + 2 * k], w1 = x[j + 2 * k + 1];
               hi[k] = qb_half2(w0, w1);
               const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
-              const float2 r = f2up(f2sub(f2pk(w0, w1), f2pk(back.x, back.y)));
+              const float2 r = f2up(f2mul(f2sub(f2pk(w0, w1), f2pk(back.x, back.y)), f2pk(QB_LO_UP, QB_LO_UP)));
               lo[k] = qb_half2(r.x, r.y);
             }
             const int c = (col0 + j) >> 3;
@@ -1291,7 +1304,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
                 float low[NH];
                 qb_tmem_ld<NH>(tmem + lanes + T_O + 64 * buf + N + c * NH, low);
 #pragma unroll
-                for (int j = 0; j < NH; ++j) o[j] += low[j];
+                for (int j = 0; j < NH; ++j) o[j] = fmaf(low[j], QB_LO_DOWN, o[j]);
               }
               if (sh.moved[i & 3][c]) {
 #pragma unroll
@@ -1446,7 +1459,8 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
             for (int p = 0; p < PARTS; ++p)
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                tc_mma_f16_ts(d, av + 8 * k, (PAIR || p ? hi : lo) + k * (2048 >> 4), I_PV, p + k > 0);
+                if (k == 0 && p) tc_mma_f16_ts<QB_LO_SHIFT>(d, av, hi, I_PV, true);
+                else tc_mma_f16_ts(d, av + 8 * k, (PAIR || p ? hi : lo) + k * (2048 >> 4), I_PV, p + k > 0);
             tc_commit(&sh.o_done[buf]);
           }
           __syncwarp();
