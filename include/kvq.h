@@ -370,7 +370,7 @@ kvq_status kvq_cross_attention(const kvq_layout* layout, int n_seqs, int n_q_tot
  *   accepted:   int32 [n_seqs][max_accept], strictly increasing draft indices, a root-to-leaf path
  *   n_accepted: int32 [n_seqs], each <= max_accept and <= n
  *   slot_map:   int64 [n_q_total], the drafts' slots (from kvq_plan_pages)
- *   seq_lens, new_lens: int32 [n_seqs] (not the same array); new_lens is written
+ *   seq_lens, new_lens: int32 [n_seqs]; new_lens is written and overlaps neither seq_lens nor cu_q, accepted, n_accepted
  *   pool:       in place
  * A path that is not valid is flagged and taken as empty; a slot outside the pool is flagged and its move left out. */
 kvq_status kvq_tree_commit(const kvq_layout* layout, int n_seqs, int n_q_total, int max_accept, const int32_t* cu_q,

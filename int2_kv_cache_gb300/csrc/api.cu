@@ -111,6 +111,12 @@ kvq::PageGeom geom(const kvq_layout* L) {
                        72 * L->page_tokens};
 }
 
+// Whether two int32 arrays share memory.
+bool overlap(const int32_t* a, long long n_a, const int32_t* b, long long n_b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * n_b && y < x + 4 * n_a;
+}
+
 #define KVQ_CHECK(expr)             \
   do {                              \
     kvq_status st_ = (expr);        \
@@ -756,7 +762,10 @@ kvq_status kvq_tree_commit(const kvq_layout* layout, int n_seqs, int n_q_total, 
   if (n_q_total > 0) KVQ_PTR(slot_map, "slot_map");
   KVQ_IDX(seq_lens, "seq_lens");
   KVQ_IDX(new_lens, "new_lens");
-  if (seq_lens == new_lens) return fail(KVQ_EINVAL, "seq_lens and new_lens must not alias");
+  if (overlap(new_lens, n_seqs, seq_lens, n_seqs) || overlap(new_lens, n_seqs, n_accepted, n_seqs) ||
+      overlap(new_lens, n_seqs, cu_q, (long long)n_seqs + 1) ||
+      (max_accept > 0 && overlap(new_lens, n_seqs, accepted, (long long)n_seqs * max_accept)))
+    return fail(KVQ_EINVAL, "new_lens must not overlap seq_lens, n_accepted, cu_q or accepted");
   KVQ_PTR(pool, "pool");
   unsigned* err = nullptr;
   KVQ_CHECK(device_error_word(&err));

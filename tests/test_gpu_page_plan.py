@@ -296,3 +296,28 @@ def test_a_captured_grow_commit_shrink_step_replays(n):
         for name, g, w in (("table", table, p.table), ("ring", ring, p.ring), ("counters", pairs[0], [p.head, p.tail]),
                            ("lens", lens, at), ("slots", slots, s), ("pool", d_pool, pool)):
             np.testing.assert_array_equal(g.cpu().numpy(), w, err_msg=name)
+
+
+def test_commit_with_its_arrays_side_by_side_in_one_buffer():
+    import oracle
+    kvq, torch, rng = gu.kvq_lib(), gu.torch_cuda(), np.random.default_rng(10)
+    page, h, ns, paths = 8, 3, [5, 9, 4], [[1, 2, 4], [], [0, 2]]
+    n, total, most = 3, sum(ns), 3
+    cu, blocks = np.concatenate([[0], np.cumsum(ns)]), 4
+    acc = np.array([x + [7] * (most - len(x)) for x in paths])
+    n_acc, lens = np.array([len(x) for x in paths]), np.array(ns) + 20
+    slots = rng.permutation(blocks * page)[:total].astype(np.int64)
+    pool = rng.integers(0, 256, blocks * h * 72 * page, dtype=np.uint8)
+    buf = gu.dev_i32(np.concatenate([cu, acc.ravel(), [-1] * n, n_acc, lens]))
+    at = np.cumsum([0, n + 1, n * most, n, n, n])
+    d_cu, d_acc, new, d_n_acc, d_lens = (buf[i:j] for i, j in zip(at, at[1:]))
+    d = torch.from_numpy(pool.copy()).cuda()
+    kvq.kvq_tree_commit(kvq.make_layout(page, h, h, blocks, 1), d_cu, d_acc.view(n, most), d_n_acc,
+                        torch.from_numpy(slots).cuda(), d_lens, new, d)
+    kvq.kvq_device_check()
+    want, want_lens = oracle.tree.commit(pool, h, page, cu, acc, n_acc, slots, lens)
+    assert np.array_equal(d.cpu().numpy(), want)
+    assert np.array_equal(new.cpu().numpy(), want_lens)
+    with pytest.raises(kvq.KvqError, match="overlap"):
+        kvq.kvq_tree_commit(kvq.make_layout(page, h, h, blocks, 1), d_cu, d_acc.view(n, most), d_n_acc,
+                            torch.from_numpy(slots).cuda(), d_lens, d_n_acc, d)

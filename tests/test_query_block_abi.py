@@ -136,3 +136,13 @@ def test_binding_rejects_types_shapes_and_host_tensors(kvq):
     with pytest.raises((TypeError, ValueError)):
         kvq.kvq_tree_attention(lay, torch.zeros(4, 32, 128), z(2), 4, None, z(1), 16, z(1, 10), kvq.DeviceRot("identity"),
                                z(9, dt=torch.uint8), z(9, dt=torch.uint8), torch.zeros(4, 32, 128))
+
+
+def test_commit_rejects_new_lens_over_its_inputs(kvq):
+    """The warps of a sequence read the path and its length on their own while one writes new_lens."""
+    lay = _layout(kvq)
+    far = dict(cu=FAKE, acc=FAKE + 0x1000, n_acc=FAKE + 0x2000, lens=FAKE + 0x3000, slots=FAKE + 0x4000, pool=FAKE + 0x8000)
+    for name, size in (("cu", 5), ("acc", 12), ("n_acc", 4), ("lens", 4)):  # entries: 4 sequences, paths of up to 3
+        for at in (far[name], far[name] + 4 * (size - 1), far[name] - 12):
+            assert _commit(kvq, lay, **far, new=at) == kvq.KVQ_EINVAL, (name, at - far[name])
+            assert b"overlap" in kvq.lib().kvq_last_error()
