@@ -312,8 +312,8 @@ kvq_status kvq_plan_workspace_size(int n_seqs, size_t* bytes);
  *   ring_out:  int64 [2] (written; not ring_in): head + pages taken, tail + pages given back
  *   block_table: int32 [n_seqs][max_blocks_per_seq], in place: taken pages are written in (sequence, page) order from
  *              the head on; given pages go to the tail in the same order, and their entries (as all others) keep their value
- *   cu_new:    int32 [n_seqs + 1] (written): running sum of max(0, new - old), ready for kvq_quantize_append
- *              (start_pos = old_lens) and as cu_q of kvq_tree_attention
+ *   cu_new:    int32 [n_seqs + 1] (written; overlaps neither old_lens nor new_lens): running sum of max(0, new - old),
+ *              ready for kvq_quantize_append (start_pos = old_lens) and as cu_q of kvq_tree_attention
  *   slot_map:  int64 [max_new] (written; may be NULL if max_new is 0): new token t of b, at position
  *              pos = old_lens[b] + t - cu_new[b], has slot page * page_tokens + pos % page_tokens of the pool;
  *              -1 from cu_new[n_seqs] on

@@ -670,6 +670,8 @@ kvq_status kvq_plan_pages(const kvq_layout* layout, int n_seqs, const int32_t* o
   KVQ_PTR(ring_out, "ring_out");
   if (ring_in == ring_out) return fail(KVQ_EINVAL, "ring_in and ring_out must not alias");
   KVQ_IDX(cu_new, "cu_new");
+  if (overlap(cu_new, (long long)n_seqs + 1, old_lens, n_seqs) || overlap(cu_new, (long long)n_seqs + 1, new_lens, n_seqs))
+    return fail(KVQ_EINVAL, "cu_new must not overlap old_lens or new_lens");
   if (max_new > 0) KVQ_PTR(slot_map, "slot_map");
   KVQ_PTR(workspace, "workspace");
   if (workspace_bytes < need) return fail(KVQ_EINVAL, "workspace %zu bytes < %zu required", workspace_bytes, need);

@@ -146,3 +146,14 @@ def test_commit_rejects_new_lens_over_its_inputs(kvq):
         for at in (far[name], far[name] + 4 * (size - 1), far[name] - 12):
             assert _commit(kvq, lay, **far, new=at) == kvq.KVQ_EINVAL, (name, at - far[name])
             assert b"overlap" in kvq.lib().kvq_last_error()
+
+
+def test_plan_rejects_cu_new_over_the_lengths(kvq):
+    """Every block reads the lengths on its own while cu_new is written."""
+    lay = _layout(kvq)
+    far = dict(old=FAKE, new=FAKE + 0x1000, table=FAKE + 0x2000, ring=FAKE + 0x3000, rin=FAKE + 0x4000, rout=FAKE + 0x5000,
+               slots=FAKE + 0x6000, ws=FAKE + 0x8000)
+    for name in ("old", "new"):
+        for at in (far[name], far[name] + 12, far[name] - 16):  # 4 lengths, 5 entries of cu_new
+            assert _plan(kvq, lay, **far, cu=at) == kvq.KVQ_EINVAL, (name, at - far[name])
+            assert b"overlap" in kvq.lib().kvq_last_error()
