@@ -41,6 +41,7 @@ cached states.  Candidate selection:
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 from ._build import LIB as LIB_PATH
@@ -370,6 +371,22 @@ def _pool(layout: KvqLayout, pool, dev: int):
     return _dense(pool, "pool", torch.uint8, None, dev)
 
 
+def _rot(layout: KvqLayout, rot: DeviceRot, dev: int) -> KvqRot:
+    """A key rotation of (at least) every KV head, which the kernels index as dense fp32."""
+    import torch
+
+    def of_heads(t, name, *each):
+        if t is None:
+            raise ValueError(f"{name} is missing")
+        if t.numel() < layout.n_kv_heads * math.prod(each):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, the layout needs {(layout.n_kv_heads, *each)}")
+        return _dense(t, name, torch.float32, None, dev)
+
+    signs = of_heads(rot.signs, "rot_k.signs", HEAD_DIM) if rot.kind == "signed_hadamard" else None
+    dense = of_heads(rot.dense, "rot_k.dense", HEAD_DIM, HEAD_DIM) if rot.kind == "dense" else None
+    return KvqRot(ROT_KIND[rot.kind], signs, dense)
+
+
 def kvq_plan_workspace_size(n_seqs: int) -> int:
     out = ctypes.c_size_t(0)
     _check(lib().kvq_plan_workspace_size(n_seqs, ctypes.byref(out)))
@@ -411,13 +428,13 @@ def kvq_tree_attention(layout: KvqLayout, q, cu_q, max_q: int, parents, seq_lens
     i32 = torch.int32
     dev, raw = _device_and_stream(stream)
     n, total = seq_lens.shape[0], q.shape[0]
-    rows = (total, layout.n_q_heads, HEAD_DIM)
+    rows, rot = (total, layout.n_q_heads, HEAD_DIM), _rot(layout, rot_k, dev)
     _check(lib().kvq_tree_attention(
         ctypes.byref(layout), n, total, _dense(q, "q", q.dtype, rows, dev), _dtype_code(q),
         _dense(cu_q, "cu_q", i32, (n + 1,), dev), max_q,
         None if parents is None else _dense(parents, "parents", i32, (total,), dev),
         _dense(seq_lens, "seq_lens", i32, (n,), dev), max_seq_len,
-        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq), dev), rot_k.c,
+        _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq), dev), rot,
         _pool(layout, pool, dev), _dense(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
         _dense(o_rot, "o_rot", torch.float32, rows, dev), raw))
 
@@ -429,11 +446,11 @@ def kvq_cross_attention(layout: KvqLayout, q, cu_q, max_q: int, state_lens, max_
     i32 = torch.int32
     dev, raw = _device_and_stream(stream)
     n, total = state_lens.shape[0], q.shape[0]
-    rows = (total, layout.n_q_heads, HEAD_DIM)
+    rows, rot = (total, layout.n_q_heads, HEAD_DIM), _rot(layout, rot_k, dev)
     _check(lib().kvq_cross_attention(
         ctypes.byref(layout), n, total, _dense(q, "q", q.dtype, rows, dev), _dtype_code(q),
         _dense(cu_q, "cu_q", i32, (n + 1,), dev), max_q, _dense(state_lens, "state_lens", i32, (n,), dev),
-        max_state_len, _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq), dev), rot_k.c,
+        max_state_len, _dense(block_table, "block_table", i32, (n, layout.max_blocks_per_seq), dev), rot,
         _pool(layout, pool, dev), _dense(workspace, "workspace", torch.uint8, None, dev), workspace.numel(),
         _dense(o_rot, "o_rot", torch.float32, rows, dev), raw))
 

@@ -157,3 +157,34 @@ def test_plan_rejects_cu_new_over_the_lengths(kvq):
         for at in (far[name], far[name] + 12, far[name] - 16):  # 4 lengths, 5 entries of cu_new
             assert _plan(kvq, lay, **far, cu=at) == kvq.KVQ_EINVAL, (name, at - far[name])
             assert b"overlap" in kvq.lib().kvq_last_error()
+
+
+@pytest.mark.parametrize("name", ["kvq_tree_attention", "kvq_cross_attention"])
+def test_binding_rejects_rotations_of_other_types_and_shapes(kvq, name):
+    """The kernels index a rotation by KV head, as fp32: one of fewer heads, or of another type, is read wrongly."""
+    torch = pytest.importorskip("torch")
+    lay = _layout(kvq)
+    i32, u8 = torch.int32, torch.uint8
+    z = lambda *s, dt=i32: torch.zeros(*s, dtype=dt)  # noqa: E731
+
+    def call(rot):
+        mid = (None,) if name == "kvq_tree_attention" else ()
+        getattr(kvq, name)(lay, torch.zeros(4, 32, 128), z(2), 4, *mid, z(1), 16, z(1, 10), rot, z(8 * 16 * 72 * 100, dt=u8),
+                           z(9, dt=u8), torch.zeros(4, 32, 128))
+
+    f64, ones = torch.float64, torch.ones
+    for rot in (kvq.DeviceRot("signed_hadamard", signs=ones(8, 128, dtype=f64)),
+                kvq.DeviceRot("dense", dense=ones(8, 128, 128, dtype=torch.bfloat16))):
+        with pytest.raises(TypeError, match="rot_k"):
+            call(rot)
+    for rot in (kvq.DeviceRot("signed_hadamard", signs=ones(1, 128)), kvq.DeviceRot("signed_hadamard", signs=ones(7, 128)),
+                kvq.DeviceRot("dense", dense=ones(1, 128, 128)), kvq.DeviceRot("dense", dense=ones(8, 128))):
+        with pytest.raises(ValueError, match="rot_k.* has shape"):
+            call(rot)
+    for rot in (kvq.DeviceRot("signed_hadamard"), kvq.DeviceRot("dense", signs=ones(8, 128))):
+        with pytest.raises(ValueError, match="rot_k"):
+            call(rot)
+    with pytest.raises(ValueError, match="not on the current CUDA device"):
+        call(kvq.DeviceRot("dense", dense=ones(8, 128, 128)))
+    with pytest.raises(ValueError, match="contiguous|not on the current"):
+        call(kvq.DeviceRot("dense", dense=ones(128, 128, 8).permute(2, 0, 1)))
