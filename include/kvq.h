@@ -322,7 +322,7 @@ kvq_status kvq_plan_workspace_size(int n_seqs, size_t* bytes);
  * [0, max_blocks_per_seq * page_tokens], too few free pages, counters out of range, more new tokens than max_new, more
  * free pages than num_blocks) changes nothing: cu_new is all 0, slot_map all -1, ring_out = ring_in, and
  * kvq_device_check reports it.  A page id outside the pool is passed on as it is and flagged; its slots are -1.
- * n_seqs <= 65535; max_new >= 0. */
+ * 1 <= n_seqs <= 65535; max_new >= 0. */
 kvq_status kvq_plan_pages(const kvq_layout* layout, int n_seqs, const int32_t* old_lens, const int32_t* new_lens,
                           int32_t* block_table, int32_t* free_ring, const int64_t* ring_in, int64_t* ring_out,
                           int max_new, int32_t* cu_new, int64_t* slot_map, void* workspace, size_t workspace_bytes,
@@ -346,6 +346,8 @@ kvq_status kvq_query_block_workspace_size(const kvq_layout* layout, int n_seqs, 
  *   seq_lens: int32 [n_seqs], the cached tokens with the drafts; max_seq_len (host) >= every seq_lens[b]
  *   o_rot:    float [n_q_total][n_q_heads][128] (written)
  *   workspace: >= kvq_query_block_workspace_size bytes, 16-byte aligned; one call at a time may use it
+ * A record of scale 0 holds codes 0, as the append writes it (a value's code c would count as c 2^-24 there).  Rows are
+ * independent: a query, however large, changes no other row's precision; infinities and NaN stay in their row.
  * Results do not depend on timing.  Sequences with inconsistent lengths and out-of-range block ids are flagged
  * (kvq_device_check) and their outputs are unspecified; a bad parent is flagged and taken as -1.
  * n_seqs <= 65535; max_seq_len <= 2^31 - 257; query heads per KV head 1, 2, 4 or 8. */
