@@ -22,9 +22,11 @@
 // term cancels, and with it the accumulators' rounding).  The fp32 operands q' and
 // w = p s enter as two fp16 halves (hi, and the remainder), 22 bits together: at 64
 // rows one after the other into one accumulator, the remainders first, below that
-// side by side as 2 N columns.  Each 128-token product starts from zero and is added
-// up in fp32 registers, so no long sum runs through the tensor cores' own rounding
-// (readouts 3 - 5e-7 off fp64).
+// side by side as 2 N columns.  A row's q' is scaled by a power of two that is the
+// tile's or, beside rows more than 2^16 as large, its own; the remainder of w is held
+// times 2^11, so that w reaches 2^-39 of the row's largest.  Each 128-token product
+// starts from zero and is added up in fp32 registers, so no long sum runs through the
+// tensor cores' own rounding (readouts 3 - 5e-7 off fp64).
 // Softmax weights are kept as w = 2^(a + log2 s - M) directly, p = w / s: fp16 then
 // holds w whatever the value scales are (a constant group, s = 0, takes the
 // smallest fp16 as s: its codes are 0 and mid compensates exactly).  M is a lazy
@@ -43,13 +45,14 @@
 // CTA is written out at once, a cut one leaves partials (numerator, l, M) that
 // qb_combine_kernel joins in slice order (results do not depend on timing).
 //
-// Bound: the instruction stream of the softmax and expansion warps.  16 trees of 32
-// drafts on 16,384 tokens, 32 / 8 heads: 357 us for the call, 386 TFLOP/s of attention
-// (0.20 of the measured cuBLAS bf16 rate, twice that as issued), a 64 x 128 tile in
-// 1.6 us, the tensor pipe active 36 %, the schedulers issuing 59 % of the time.  The
-// roles run side by side from one instruction cache, so their common path is kept
-// short: with the expansion loops unrolled the same call takes 414 us, with
-// everything unrolled 1,446 us.
+// Bound: no unit is full.  16 trees of 32 drafts on 16,384 tokens, 32 / 8 heads: 360 us
+// for the call, 382 TFLOP/s of attention (0.20 of the measured cuBLAS bf16 rate, twice
+// that as issued), a 64 x 128 tile in 1.6 us, the tensor pipe active 36 %, the schedulers
+// issuing 60 % of the time; the largest stall is the long scoreboard (3.85 warps an
+// issue).  The time is in the chain of waits from role to role; which role holds the
+// others up has not been measured.  The roles run side by side from one instruction
+// cache, so their common path is kept short: with the expansion loops unrolled the same
+// call took 414 us (then 357), with everything unrolled 1,446 us.
 #include <algorithm>
 #include <cstddef>
 
@@ -66,12 +69,12 @@ constexpr int QB_STAGE_BYTES = QB_TOK * 72;
 constexpr int QB_PBUF = QB_TOK * 128;             // one half of W^T: 128 rows of 128 bytes (64 fp16 columns)
 constexpr int QB_UNITS = 4;                       // ring of unit descriptors
 constexpr int QB_UNIT_WORK = 3;                   // what starting and ending a unit costs, in tiles (measured: 5 us and 1.6 us)
-// Weights: the running maximum is put at 2^3 (further from fp16's smallest step than at 1: readout error 6.5e-7 -> 4.6e-7,
-// the same at 2^6), and again whenever a weight would pass 2^15.5.
+// Weights: the running maximum is put at 2^3 (further from fp16's smallest step than at 1: with the second half unscaled,
+// readout error 6.5e-7 -> 4.6e-7, the same at 2^6), and again whenever a weight would pass 2^15.5.
 constexpr float QB_LIFT = 3.f, QB_TRIGGER = 15.5f;
 // A weight's second half is held times 2^11: up to half a step of the largest weight (2^15), and down to 2^-36 in all.
-// Unscaled, weights ended at fp16's 2^-25, 2^-28 of the largest: behind a token 19 nats above 131,071 others, a third of
-// a per mille of the readout was lost.
+// Unscaled, weights ended at fp16's 2^-25, 2^-28 of the largest: behind a token 16 to 22 nats above 131,071 others, the
+// readout was up to 7e-4 off.
 constexpr int QB_LO_SHIFT = 11;
 constexpr float QB_LO_UP = 2048.f, QB_LO_DOWN = 1.f / 2048.f;
 
@@ -729,7 +732,6 @@ __device__ __forceinline__ uint32_t qb_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// A token's constants: key scale and mid, log2 of the value scale, its reciprocal, value mid over value scale.
 // A vote of four warps at hardware barrier `id`.
 __device__ __forceinline__ bool qb_vote(int id, bool p) {
   uint32_t any;
@@ -740,6 +742,7 @@ __device__ __forceinline__ bool qb_vote(int id, bool p) {
       : "memory");
   return any != 0;
 }
+// A token's constants: key scale and mid, log2 of the value scale, its reciprocal, value mid over value scale.
 enum { QB_C_SK, QB_C_KMID, QB_C_LS, QB_C_INV, QB_C_ZC };
 
 // Register shares by role (a thread; 0: as launched): keys, values, softmax, accumulation, copies and MMA issue.  The
