@@ -27,7 +27,9 @@
 // 256 tokens the sums go to fp32 sums in tensor memory, which nothing else here uses (at 16,384
 // tokens 2.7e-6 -> 1.2e-6 off, 59.5 -> 61.8 us; every 512 tokens 1.7e-6, 61.5 us).  The weights
 // change from a lane a token to a lane a column by matrix transposes (shuffles and selections
-// instead: 2 us more).
+// instead: 2 us more).  A weight times its value scale has to fit fp16: the reference that scores
+// are taken from moves when it does not (scales over 512), and lies below the maximum where all
+// scales are tiny (ds_lift); looking at it in every chunk costs 0.4 of 63 us.
 //
 // Bound: a warp's chain of products, fields and weights, four warps a scheduler (58 % of the
 // issue slots; without the work the call takes 39 us, without the copies alone 61, without
@@ -48,6 +50,7 @@ constexpr float DS_LOG2E = 1.4426950408889634f;
 constexpr int DS_STAGES = 3;
 constexpr float DS_TAU = 6.f;        // a reference maximum moves once a score passes it by 2^6
 constexpr float DS_LO = 2048.f;      // second halves are held times 2^11
+constexpr float DS_HIGH = 32768.f;   // a weight times its value scale above this moves the reference too
 constexpr int DS_PART = D + 4;       // acc[128], m (base 2), l, 2 unused
 constexpr int DS_PREP_THREADS = 256;
 
@@ -127,6 +130,23 @@ __device__ __forceinline__ DsView ds_view(const DsArgs& a, int b, unsigned* err 
 __device__ __forceinline__ uint32_t ds_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// How far the reference lies below the maximum where the largest weight times its value scale is 2^most: that one goes as fp16
+// halves and is brought to 2^-8 .. 2^9, where both keep their bits and scores 2^6 above the maximum stay in range.  0 for
+// the scales of most caches; 40 at most, so that sums of weights and zeros stay far from fp32's ends.
+__device__ __forceinline__ float ds_lift(float most) {
+  const float e = floorf(most);
+  return e > 8.f ? 8.f - e : e < -8.f ? fminf(-8.f - e, 40.f) : 0.f;
+}
+__device__ __forceinline__ float ds_lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ds_max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 __device__ __forceinline__ float ds_ex2(float x) {
   float y;
@@ -574,15 +594,38 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
     uint32_t bp[NT][2][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float top = fmaxf(fmaxf(x[nt][0], x[nt][1]), fmaxf(x[nt][2], x[nt][3]));
-      if (__any_sync(FULL, top > thr[nt])) {
-        float mx = fmaxf(top, __shfl_xor_sync(FULL, top, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 16));
-        if (mx > thr[nt]) {
-          const float scale = thr[nt] == -INFINITY ? 0.f : ds_ex2(m[nt] - mx);
-          m[nt] = mx;
-          thr[nt] = mx + DS_TAU;
+      const float top = ds_max3(x[nt][0], x[nt][1], fmaxf(x[nt][2], x[nt][3]));
+      float p[4], w[4];  // 2^(x - ref), the same times the value scale; the largest of these
+      auto weigh = [&](float ref) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          p[k] = ds_ex2(x[nt][k] - ref);
+          w[k] = p[k] * vs[k];
+          if (!ALL) {
+            p[k] = seen[k] ? p[k] : 0.f;
+            w[k] = seen[k] ? w[k] : 0.f;
+          }
+        }
+        return ds_max3(fabsf(w[0]), fabsf(w[1]), fmaxf(fabsf(w[2]), fabsf(w[3])));
+      };
+      const float high = weigh(m[nt]);
+      const bool rises = top > thr[nt], over = high > DS_HIGH;
+      if (__any_sync(FULL, rises || over)) {
+        const unsigned column = 0x11111111u << ti;  // of heads: 32 tokens
+        const unsigned up = __ballot_sync(FULL, rises) & column, far = __ballot_sync(FULL, over) & column;
+        float mx = top, most = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = fmaxf(most, x[nt][k] + ds_lg2(fabsf(vs[k])));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+          most = fmaxf(most, __shfl_xor_sync(FULL, most, o));
+        }
+        if (up | far) {
+          const float ref = up ? mx : thr[nt] - DS_TAU, now = ref - ds_lift(most - ref);
+          const float scale = thr[nt] == -INFINITY ? 0.f : ds_ex2(m[nt] - now);
+          m[nt] = now;
+          thr[nt] = ref + DS_TAU;
           behind[nt] *= scale;
           lp[nt] *= scale;
           zp[nt] *= scale;
@@ -591,20 +634,17 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
             acc[nt][f][0] *= scale; acc[nt][f][1] *= scale; acc[nt][f][2] *= scale; acc[nt][f][3] *= scale;
           }
         }
+        weigh(m[nt]);
       }
       uint32_t pk[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float p = ds_ex2(x[nt][k] - m[nt]), w = p * vs[k], z = p * vz[k];
-        if (!ALL) {
-          p = seen[k] ? p : 0.f;
-          w = seen[k] ? w : 0.f;
-          z = seen[k] ? z : 0.f;
-        }
-        lp[nt] += p;
+        float z = p[k] * vz[k];
+        if (!ALL) z = seen[k] ? z : 0.f;
+        lp[nt] += p[k];
         zp[nt] += z;
-        const float hf = __half2float(__float2half_rn(w));
-        pk[k] = ds_half2(w, (w - hf) * DS_LO);
+        const float hf = __half2float(__float2half_rn(w[k]));
+        pk[k] = ds_half2(w[k], (w[k] - hf) * DS_LO);
       }
       // lane (g, t) has token g of head 4 nt + t, first half and remainder; the product wants columns g, tokens 2 t, 2 t + 1
 #pragma unroll
