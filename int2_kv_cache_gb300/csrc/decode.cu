@@ -43,7 +43,11 @@
 // fp32 operand of each product (the rotated query, the weights p_t s_t) is
 // split into an fp16 high part and an fp16 remainder occupying the two MMA
 // columns of one head, which keeps ~22 significant bits.  The softmax runs
-// online in base 2 with a lazy reference maximum.
+// online in base 2 with a lazy reference maximum, which also moves when a weight
+// times its value scale leaves fp16's range (weight_lift).  Looking at the weights
+// of every chunk costs a step of 16 x 32,768 tokens 1.1 of 101.6 us, one of 131,072
+// 1.1 of 43.4; a second look at slices whose sums are not finite, in the combine
+// instead, 0.6 and 0.6, but 64 sequences of up to 8,192 1.7 of 116.8 (here 0.2).
 #include <type_traits>
 
 #include "async_copy.cuh"
@@ -844,7 +848,7 @@ __global__ void __launch_bounds__(dec_max_warps(G) * 32, 1) decode_split_kernel(
 
   // ---- per-segment state (one segment = the warp's entries of one unit) ----
   uint32_t bq[NT][8][2];  // B fragments of q'.c, k-slice s (see qprep_kernel)
-  float dsc[NT], qsum_s[NT], tau_s[NT], m_s[NT], thr[NT], nm[NT], lp[NT], zp[NT];
+  float dsc[NT], qsum_s[NT], tau_s[NT], thr[NT], nm[NT], lp[NT], zp[NT];
   float acc[NT][8][4];
   int cur_u = -1, cur_S = 0, cur_E = 0;
 
@@ -865,7 +869,6 @@ __global__ void __launch_bounds__(dec_max_warps(G) * 32, 1) decode_split_kernel(
       dsc[nt] = c.x;
       qsum_s[nt] = c.y;
       tau_s[nt] = c.z;
-      m_s[nt] = -INFINITY;
       thr[nt] = -INFINITY;
       nm[nt] = 0.f;
       lp[nt] = 0.f;
@@ -903,7 +906,7 @@ __global__ void __launch_bounds__(dec_max_warps(G) * 32, 1) decode_split_kernel(
         dst[16 + 2 * gi] = make_float4(o[8], o[9], o[10], o[11]);
         dst[16 + 2 * gi + 1] = make_float4(o[12], o[13], o[14], o[15]);
         if (gi == 0) {
-          pp[j * PART + D] = m_s[nt] * dsc[nt];
+          pp[j * PART + D] = thr[nt] == -INFINITY ? -INFINITY : -nm[nt];
           pp[j * PART + D + 1] = lp[nt];
         }
       }
@@ -970,40 +973,57 @@ __global__ void __launch_bounds__(dec_max_warps(G) * 32, 1) decode_split_kernel(
     uint32_t bp[NT][2][2];  // [n-tile][tile][b register]
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float lm = fmaxf(fmaxf(sc[nt][0], sc[nt][1]), fmaxf(sc[nt][2], sc[nt][3]));
-      if (__any_sync(FULLM, lm > thr[nt])) {  // some head's maximum moved by > TAU
-        float mx = fmaxf(lm, __shfl_xor_sync(FULLM, lm, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(FULLM, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(FULLM, mx, 16));
-        const bool need = mx > thr[nt];
-        const float alpha = need ? ex2((m_s[nt] - mx) * dsc[nt]) : 1.f;
-        if (need) {
-          m_s[nt] = mx;
-          thr[nt] = mx + tau_s[nt];
-          nm[nt] = -mx * dsc[nt];
-        }
-        lp[nt] *= alpha;
-        zp[nt] *= alpha;
+      const float lm = max3(sc[nt][0], sc[nt][1], fmaxf(sc[nt][2], sc[nt][3]));
+      float p[4], w[4];  // weights, and times the value scale
+      auto weigh = [&]() {
 #pragma unroll
-        for (int f = 0; f < 8; ++f) {
-          acc[nt][f][0] *= alpha; acc[nt][f][1] *= alpha; acc[nt][f][2] *= alpha; acc[nt][f][3] *= alpha;
+        for (int k = 0; k < 4; ++k) {
+          p[k] = ex2(fmaf(sc[nt][k], dsc[nt], nm[nt]));
+          w[k] = p[k] * vsx[k];
+          if (!FULL) {
+            p[k] = rok[k] ? p[k] : 0.f;
+            w[k] = rok[k] ? w[k] : 0.f;
+          }
         }
+      };
+      weigh();
+      const bool rises = lm > thr[nt];
+      const bool over = max3(fabsf(w[0]), fabsf(w[1]), fmaxf(fabsf(w[2]), fabsf(w[3]))) > WEIGHT_HIGH;
+      if (__any_sync(FULLM, rises || over)) {  // some head's maximum moved by > TAU, or a weight left fp16's range
+        const unsigned column = 0x11111111u << ti;  // the lanes of a head: 32 tokens
+        const unsigned up = __ballot_sync(FULLM, rises) & column, far = __ballot_sync(FULLM, over) & column;
+        float mx = lm, most = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = fmaxf(most, fmaf(sc[nt][k], dsc[nt], lg2_approx(fabsf(vsx[k]))));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(FULLM, mx, o));
+          most = fmaxf(most, __shfl_xor_sync(FULLM, most, o));
+        }
+        if (up | far) {
+          const float ref = up ? mx : thr[nt] - tau_s[nt];
+          const float now = -ref * dsc[nt] + weight_lift(fmaf(-ref, dsc[nt], most));
+          const float alpha = thr[nt] == -INFINITY ? 0.f : ex2(now - nm[nt]);
+          thr[nt] = ref + tau_s[nt];
+          nm[nt] = now;
+          lp[nt] *= alpha;
+          zp[nt] *= alpha;
+#pragma unroll
+          for (int f = 0; f < 8; ++f) {
+            acc[nt][f][0] *= alpha; acc[nt][f][1] *= alpha; acc[nt][f][2] *= alpha; acc[nt][f][3] *= alpha;
+          }
+        }
+        weigh();
       }
       uint32_t pk[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float p = ex2(fmaf(sc[nt][k], dsc[nt], nm[nt]));
-        float w = p * vsx[k];
-        float pz = p * vzz[k];
-        if (!FULL) {
-          p = rok[k] ? p : 0.f;
-          w = rok[k] ? w : 0.f;
-          pz = rok[k] ? pz : 0.f;
-        }
-        lp[nt] += p;
+        float pz = p[k] * vzz[k];
+        if (!FULL) pz = rok[k] ? pz : 0.f;
+        lp[nt] += p[k];
         zp[nt] += pz;
-        const float hf = half_rn(w);
-        pk[k] = pack_half2(w, (w - hf) * LO_SCALE);  // low half: fp16(w); high half: remainder * 2^11
+        const float hf = half_rn(w[k]);
+        pk[k] = pack_half2(w[k], (w[k] - hf) * LO_SCALE);  // low half: fp16(w); high half: remainder * 2^11
       }
       // B fragment of tile u: k = 2t, 2t+1, 2t+8, 2t+9 <-> tokens 2t, 2t+1, 2t+8, 2t+9;
       // column g <-> head 4nt + g/2, high part (g even) or remainder (g odd)

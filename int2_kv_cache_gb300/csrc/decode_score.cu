@@ -29,7 +29,7 @@
 // change from a lane a token to a lane a column by matrix transposes (shuffles and selections
 // instead: 2 us more).  A weight times its value scale has to fit fp16: the reference that scores
 // are taken from moves when it does not (scales over 512), and lies below the maximum where all
-// scales are tiny (ds_lift); looking at it in every chunk costs 0.4 of 63 us.
+// scales are tiny (weight_lift); looking at it in every chunk costs 0.4 of 63 us.
 //
 // Bound: a warp's chain of products, fields and weights, four warps a scheduler (58 % of the
 // issue slots; without the work the call takes 39 us, without the copies alone 61, without
@@ -50,7 +50,6 @@ constexpr float DS_LOG2E = 1.4426950408889634f;
 constexpr int DS_STAGES = 3;
 constexpr float DS_TAU = 6.f;        // a reference maximum moves once a score passes it by 2^6
 constexpr float DS_LO = 2048.f;      // second halves are held times 2^11
-constexpr float DS_HIGH = 32768.f;   // a weight times its value scale above this moves the reference too
 constexpr int DS_PART = D + 4;       // acc[128], m (base 2), l, 2 unused
 constexpr int DS_PREP_THREADS = 256;
 
@@ -130,23 +129,6 @@ __device__ __forceinline__ DsView ds_view(const DsArgs& a, int b, unsigned* err 
 __device__ __forceinline__ uint32_t ds_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-// How far the reference lies below the maximum where the largest weight times its value scale is 2^most: that one goes as fp16
-// halves and is brought to 2^-8 .. 2^9, where both keep their bits and scores 2^6 above the maximum stay in range.  0 for
-// the scales of most caches; 40 at most, so that sums of weights and zeros stay far from fp32's ends.
-__device__ __forceinline__ float ds_lift(float most) {
-  const float e = floorf(most);
-  return e > 8.f ? 8.f - e : e < -8.f ? fminf(-8.f - e, 40.f) : 0.f;
-}
-__device__ __forceinline__ float ds_lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float ds_max3(float a, float b, float c) {
-  float y;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
 }
 __device__ __forceinline__ float ds_ex2(float x) {
   float y;
@@ -594,7 +576,7 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
     uint32_t bp[NT][2][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float top = ds_max3(x[nt][0], x[nt][1], fmaxf(x[nt][2], x[nt][3]));
+      const float top = max3(x[nt][0], x[nt][1], fmaxf(x[nt][2], x[nt][3]));
       float p[4], w[4];  // 2^(x - ref), the same times the value scale; the largest of these
       auto weigh = [&](float ref) {
 #pragma unroll
@@ -606,23 +588,23 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
             w[k] = seen[k] ? w[k] : 0.f;
           }
         }
-        return ds_max3(fabsf(w[0]), fabsf(w[1]), fmaxf(fabsf(w[2]), fabsf(w[3])));
+        return max3(fabsf(w[0]), fabsf(w[1]), fmaxf(fabsf(w[2]), fabsf(w[3])));
       };
       const float high = weigh(m[nt]);
-      const bool rises = top > thr[nt], over = high > DS_HIGH;
+      const bool rises = top > thr[nt], over = high > WEIGHT_HIGH;
       if (__any_sync(FULL, rises || over)) {
         const unsigned column = 0x11111111u << ti;  // of heads: 32 tokens
         const unsigned up = __ballot_sync(FULL, rises) & column, far = __ballot_sync(FULL, over) & column;
         float mx = top, most = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) most = fmaxf(most, x[nt][k] + ds_lg2(fabsf(vs[k])));
+        for (int k = 0; k < 4; ++k) most = fmaxf(most, x[nt][k] + lg2_approx(fabsf(vs[k])));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
           most = fmaxf(most, __shfl_xor_sync(FULL, most, o));
         }
         if (up | far) {
-          const float ref = up ? mx : thr[nt] - DS_TAU, now = ref - ds_lift(most - ref);
+          const float ref = up ? mx : thr[nt] - DS_TAU, now = ref - weight_lift(most - ref);
           const float scale = thr[nt] == -INFINITY ? 0.f : ds_ex2(m[nt] - now);
           m[nt] = now;
           thr[nt] = ref + DS_TAU;

@@ -485,4 +485,26 @@ __device__ __forceinline__ unsigned quantize_warp_df(const DF x[4], float clip, 
   return qcode_df(x[0], qp) | (qcode_df(x[1], qp) << 2) | (qcode_df(x[2], qp) << 4) | (qcode_df(x[3], qp) << 6);
 }
 
+// ---- the reference of a decode's softmax weights ----
+// A weight 2^(a - ref) times its value scale goes to the tensor cores as fp16 halves.  Above WEIGHT_HIGH it moves the
+// reference, as a score does that passes the maximum by the lazy softmax's threshold.
+constexpr float WEIGHT_HIGH = 32768.f;
+// How far the reference lies below the maximum where the largest weight times its value scale is 2^most: that one goes as fp16
+// halves and is brought to 2^-8 .. 2^9, where both keep their bits and scores 2^6 above the maximum stay in range.  0 for
+// the scales of most caches; 40 at most, so that sums of weights and zeros stay far from fp32's ends.
+__device__ __forceinline__ float weight_lift(float most) {
+  const float e = floorf(most);
+  return e > 8.f ? 8.f - e : e < -8.f ? fminf(-8.f - e, 40.f) : 0.f;
+}
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 }  // namespace kvq
