@@ -50,6 +50,10 @@ constexpr float DS_LOG2E = 1.4426950408889634f;
 constexpr int DS_STAGES = 3;
 constexpr float DS_TAU = 6.f;        // a reference maximum moves once a score passes it by 2^6
 constexpr float DS_LO = 2048.f;      // second halves are held times 2^11
+// Scores are taken over the cap, if there is one: in units 2^k of it for a row whose scale would pass 2^60 of it, as scores
+// that fp32 can tell from 0 are then far past the cap either way.  Without a cap rows over 2^59 have theirs in units of 2^64,
+// and say so by a negative scale.  Neither a score's terms nor their scale then pass fp32.
+constexpr float DS_FAR = 0x1p64f;
 constexpr int DS_PART = D + 4;       // acc[128], m (base 2), l, 2 unused
 constexpr int DS_PREP_THREADS = 256;
 
@@ -73,7 +77,7 @@ __host__ __device__ constexpr int ds_value_bit(int f) { return 2 * f + ds_value_
 struct DsWs {
   float* part;      // [warps + units][gqa][132]: the partial of warp w for unit u at w + u
   uint32_t* qfrag;  // [units][16 * tiles][32]
-  float2* qsum;     // [units][gqa] (scale of the products, sum of q')
+  float2* qsum;     // [units][gqa] (scale of the products, sum of q'), in the row's units: see DS_FAR
   int2* span;       // [units] the slices that meet the unit
 };
 
@@ -216,13 +220,17 @@ __global__ void __launch_bounds__(DS_PREP_THREADS) ds_prepare_kernel(const __gri
     __syncthreads();
     for (int j = warp; j < G; j += NW) {
       const float4 v = reinterpret_cast<const float4*>(qv[j])[lane];
-      const float tot = warp_sum((v.x + v.y) + (v.z + v.w));
       const float mx = warp_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+      // the largest |q'| 2^e in [2^9, 2^10): 2^4 more at the lowest field stays in fp16
+      const int e = mx > 0.f && mx < INFINITY ? min(100, 9 - ilogbf(mx)) : 0;  // -119 for the largest finite row
+      const float unit = a.score.cap > 0.f ? scalbnf(a.score.inv_cap, min(0, 60 - 16 + e - ilogbf(a.score.inv_cap)))
+                         : e < -50         ? 1.f / DS_FAR
+                                           : 1.f;
+      const float tot = warp_sum((v.x * unit + v.y * unit) + (v.z * unit + v.w * unit));
       if (lane == 0) {
-        // the largest |q'| 2^e in [2^9, 2^10): 2^4 more at the lowest field stays in fp16
-        const int e = mx > 0.f && mx < INFINITY ? min(100, max(-110, 9 - ilogbf(mx))) : 0;
         s_exp[j] = e;
-        a.ws.qsum[(size_t)u * G + j] = make_float2(exp2f((float)(16 - e)), tot);
+        const float scale = scalbnf(unit, 16 - e);
+        a.ws.qsum[(size_t)u * G + j] = make_float2(a.score.cap == 0.f && e < -50 ? -scale : scale, tot);
       }
     }
     __syncthreads();
@@ -402,12 +410,14 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
   float behind[NT];      // what the sums in tensor memory are scaled by by now
   bool flushed = false;  // whether there are any
   int unit = -1, first = 0, end = 0;
-  const float cap = a.score.cap, inv_cap = a.score.inv_cap;
+  const float cap = a.score.cap;
+  unsigned far = 0;  // bit nt: the units of the lane's row there are DS_FAR
   auto begin = [&](const Place& p) {
     unit = p.b * H + p.h;
     first = p.first;
     end = p.end;
     const uint32_t* fr = a.ws.qfrag + (size_t)unit * NT * 16 * 32 + lane;
+    far = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -417,8 +427,9 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
       }
       const int j = 4 * nt + ti;
       const float2 c = j < G ? __ldg(a.ws.qsum + (size_t)unit * G + j) : make_float2(0.f, 0.f);
-      qs[nt] = c.x;
+      qs[nt] = fabsf(c.x);
       qt[nt] = c.y;
+      far |= c.x < 0.f ? 1u << nt : 0u;
       slope[nt] = a.score.slopes && j < G ? __ldg(a.score.slopes + p.h * G + j) * DS_LOG2E : 0.f;
       m[nt] = 0.f;
       thr[nt] = -INFINITY;
@@ -527,10 +538,7 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[nt][k] *= inv_cap;
-          z = fmaxf(z, x[nt][k] * x[nt][k]);
-        }
+        for (int k = 0; k < 4; ++k) z = fmaxf(z, x[nt][k] * x[nt][k]);
       if (__any_sync(FULL, z > CAP_FIT)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -547,6 +555,14 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
             x[nt][k + 1] = cap * t.y;
           }
       }
+    } else if (far) {  // scores beyond fp32's largest are equal
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float y = x[nt][k] * (far >> nt & 1 ? DS_FAR : 1.f);
+          x[nt][k] = fabsf(y) > 0x1p126f ? copysignf(0x1p126f, y) : y;
+        }
     }
     if (a.score.slopes) {
       const int far = v.len - 1 - tok0 - gi;
