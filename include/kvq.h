@@ -433,7 +433,8 @@ kvq_status kvq_read_cache(const kvq_layout* layout, int n_seqs, int n_tok_total,
 
 /* What a layer does to its scores, and what a query at position t sees:
  *   a <- cap tanh(a / cap)           cap > 0 (2^-20 .. 2^100); 0: none
- *   a <- a - slopes[j] |t - s|       slopes: float [n_q_heads] on the device, finite, in units of a; NULL: none
+ *   a <- a - slopes[j] |t - s|       slopes: float [n_q_heads] on the device, finite, in units of a; NULL: none;
+ *                                    beyond +-2^89 taken as that
  *   s is seen if (s <= t and s > t - window) or s < prefix_lens[b]
  * in this order.  window: tokens, the query's own included; 0: no limit.  prefix_lens: int32 [n_seqs] on the device,
  * or NULL: positions that every query sees, those before them too (a bidirectional prefix, or the first tokens beside a window);

@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
       qs[nt] = fabsf(c.x);
       qt[nt] = c.y;
       far |= c.x < 0.f ? 1u << nt : 0u;
-      slope[nt] = a.score.slopes && j < G ? __ldg(a.score.slopes + p.h * G + j) * DS_LOG2E : 0.f;
+      slope[nt] = a.score.slopes && j < G ? score_slope(__ldg(a.score.slopes + p.h * G + j)) : 0.f;
       m[nt] = 0.f;
       thr[nt] = -INFINITY;
       lp[nt] = zp[nt] = 0.f;

@@ -69,7 +69,6 @@
 
 namespace kvq {
 
-constexpr float QB_LOG2E = 1.4426950408889634f;
 constexpr float QB_SCALE = 0.12751742902274214f;  // log2(e) / sqrt(128): base-2 logits
 
 constexpr int QB_TOK = 128;                       // tokens a tile
@@ -1445,7 +1444,7 @@ __global__ void __launch_bounds__(QB_THREADS, 1) qb_attend_kernel(QbArgs a) {
                                : a.mode == QB_CHAIN ? tk
                                                      : 0;
             if constexpr (SCORE) {
-              if (row < 8) sh.slope[buf][row] = a.score.slopes ? -QB_LOG2E * a.score.slopes[next.h * a.gqa + (row & gm)] : 0.f;
+              if (row < 8) sh.slope[buf][row] = a.score.slopes ? -score_slope(a.score.slopes[next.h * a.gqa + (row & gm)]) : 0.f;
               sh.draft[row] = (float)(row >> gs);
               if (row == 0) {
                 const int from = next.len - next.n, first = from + next.rt * (N >> gs);

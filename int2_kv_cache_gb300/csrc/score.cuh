@@ -5,6 +5,11 @@
 
 namespace kvq {
 
+// A slope in base 2, held to where a bias of 2^31 tokens and the scores beside it stay finite.
+__device__ __forceinline__ float score_slope(float slope) {
+  return fminf(fmaxf(slope * 1.4426950408889634f, -0x1p90f), 0x1p90f);
+}
+
 // (tanh(y) / y - 1) / z, z = y^2 <= 0.64, fitted in Chebyshev points (degree 5): tanh off by 1.7e-8 of itself.
 constexpr float CAP_FIT = 0.64f;
 __host__ __device__ constexpr float tanh_fit_at(int i) {
