@@ -448,7 +448,7 @@ typedef struct {
 
 /* kvq_decode_attention with kvq_score: one query a sequence, at position seq_lens[b] - 1.  Pages that it does not see are
  * not read and their block-table entries may be anything.  Arguments, workspace (kvq_decode_workspace_size with
- * n_splits = 0), limits and errors as there; a length above max_seq_len is flagged.  Readouts are about 10^-6 of the
+ * n_splits = 0), limits and errors as there; max_seq_len <= 2^31 - 257, a length above max_seq_len is flagged.  Readouts are about 10^-6 of the
  * values' size off (kvq_decode_attention: 10^-5). */
 kvq_status kvq_decode_attention_score(const kvq_layout* layout, int n_seqs, const void* q, kvq_dtype q_dtype,
                                       const int32_t* seq_lens, int max_seq_len, const int32_t* block_table,

@@ -263,7 +263,7 @@ kvq_status kvq_window_append(const kvq_layout* layout, int n_seqs, int n_new_tot
 // Index ranges the decode kernels keep in 32-bit integers.
 static kvq_status check_decode_size(const kvq_layout* layout, int n_seqs, int max_seq_len) {
   if (n_seqs > 65535) return fail(KVQ_EUNSUPPORTED, "n_seqs %d > 65535", n_seqs);
-  const long long entries = (long long)n_seqs * layout->n_kv_heads * ((max_seq_len + 31) / 32);
+  const long long entries = (long long)n_seqs * layout->n_kv_heads * ((max_seq_len + 31ll) / 32);
   if (entries >= (1ll << 30)) return fail(KVQ_EUNSUPPORTED, "%lld cached 32-token chunks per call", entries);
   if ((long long)layout->num_blocks * layout->n_kv_heads >= (1ll << 31))
     return fail(KVQ_EUNSUPPORTED, "num_blocks * n_kv_heads >= 2^31");
@@ -884,6 +884,7 @@ kvq_status kvq_decode_attention_score(const kvq_layout* layout, int n_seqs, cons
                                       size_t workspace_bytes, float* o_rot, kvq_stream stream) {
   size_t need = 0;
   KVQ_CHECK(kvq_decode_workspace_size(layout, n_seqs, max_seq_len, 0, &need));
+  if (max_seq_len > INT32_MAX - 256) return fail(KVQ_EUNSUPPORTED, "max_seq_len %d > 2^31 - 257", max_seq_len);
   if ((long long)max_seq_len > (long long)layout->max_blocks_per_seq * layout->page_tokens)
     return fail(KVQ_EINVAL, "max_seq_len %d outside [0, max_blocks_per_seq * page_tokens]", max_seq_len);
   if (!valid_dtype(q_dtype)) return fail(KVQ_EINVAL, "bad q dtype %d", (int)q_dtype);

@@ -132,7 +132,7 @@ size_t decode_workspace_bytes(int n_seqs, int n_kv_heads, int gqa, int n_ctas, b
 // Default grid: a full single wave (4 or 3 CTAs per SM), but no more warps than
 // slices of at least four chunks.
 int decode_auto_ctas(int n_seqs, int n_kv_heads, int gqa, int max_seq_len) {
-  const long long chunks = (long long)n_seqs * n_kv_heads * ((max_seq_len + 31) / 32);
+  const long long chunks = (long long)n_seqs * n_kv_heads * ((max_seq_len + 31ll) / 32);
   const long long by_work = (chunks + 4 * DEC_WARPS - 1) / (4 * DEC_WARPS);
   long long n = (long long)device_sm_count() * ctas_per_sm(gqa);
   if (n > by_work) n = by_work;
