@@ -391,8 +391,8 @@ kvq_status kvq_tree_commit(const kvq_layout* layout, int n_seqs, int n_q_total, 
  *   rotary_dim: 0, 16, 32 .. 128 (0: no rotation); n_axes: 1 .. 4
  *   inv_freq:   HOST double [rotary_dim / 2], finite; scaled rotations pass their own
  *   axis:       HOST int32 [rotary_dim / 2], each in [0, n_axes), or NULL (axis 0)
- * Both are read during the call.  An angle is off by 2^-52 turns a position at most (a product in 64-bit fixed point), and
- * rounded to fp32 once whole turns are gone. */
+ * Both are read during the call.  An angle is off by at most 2^-64 turns a position (a product in 64-bit fixed point), beyond
+ * |inv_freq| = 2^38 by 2^-102 |inv_freq|, then cut to 2^-32 turns and rounded to fp32 once whole turns are gone. */
 typedef struct {
   int rotary_dim;
   int interleaved;

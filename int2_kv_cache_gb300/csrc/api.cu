@@ -786,6 +786,19 @@ static bool meet(const void* a, long long na, const void* b, long long nb) {
   return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
+// What a frequency of f radians a position adds to an angle, in 2^-64 turns, modulo whole ones.  1 / 2 pi stands as the sum of
+// two doubles and the product with the first is split into itself and its remainder, so that what is rounded to 2^-64 turns
+// is off by about 2^-105 f; whole turns are dropped part by part, without rounding.
+static unsigned long long turn_of(double f) {
+  const double a = std::fabs(f), up = 4294967296.0;
+  const volatile double p = a * 0x1.45f306dc9c883p-3;  // its remainder counts on this rounding
+  const double r = std::fma(a, -0x1.6b01ec5417056p-57, std::fma(a, 0x1.45f306dc9c883p-3, -p));
+  const double v = (p - std::floor(p)) * up * up, w = (r - std::nearbyint(r)) * up, whole = std::nearbyint(w);
+  const unsigned long long t = (unsigned long long)std::floor(v) + ((unsigned long long)(long long)whole << 32) +
+                               (unsigned long long)std::llrint((w - whole) * up + (v - std::floor(v)));
+  return f < 0 ? 0 - t : t;
+}
+
 kvq_status kvq_norm_rope(int n_tok, int n_q_heads, int n_kv_heads, const void* qkv, kvq_dtype dtype, int64_t row_stride,
                          const int32_t* positions, const kvq_rope* rope, const float* w_q, const float* w_k, float eps,
                          void* q, void* k, void* v, kvq_stream stream) {
@@ -812,12 +825,7 @@ kvq_status kvq_norm_rope(int n_tok, int n_q_heads, int n_kv_heads, const void* q
     if (!std::isfinite(f)) return fail(KVQ_EINVAL, "inv_freq[%d] is not finite", i);
     const int axis = rope->axis ? rope->axis[i] : 0;
     if (axis < 0 || axis >= rope->n_axes) return fail(KVQ_EINVAL, "axis[%d] = %d outside [0, n_axes)", i, axis);
-    // the fraction of a turn in [0, 1], times 2^64 (1, of a tiny negative frequency: 0)
-    const double turns = f / 6.283185307179586476925287;
-    const double frac = turns >= 0.0 && turns < 1.0 ? turns : turns - std::floor(turns);
-    const double up = frac * 4294967296.0;
-    const unsigned long long hi = (unsigned long long)up;
-    dev.turn[i] = (hi << 32) + (unsigned long long)((up - (double)hi) * 4294967296.0);
+    dev.turn[i] = turn_of(f);
     dev.axis[i] = (unsigned char)axis;
   }
   if (n_tok == 0) return KVQ_OK;

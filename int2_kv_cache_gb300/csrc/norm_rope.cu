@@ -8,7 +8,7 @@
 // Angles.  A position times a frequency in fp32 is off by up to 2^-24 of itself: 0.06
 // at position 10^6.  A frequency is therefore held as the fraction of a turn that one
 // position adds, in 64-bit fixed point: an integer product modulo 2^64 drops whole
-// turns without rounding, and what is left is off by at most 2^-65 turns a position.
+// turns without rounding, and what is left is off by 2^-64 turns a position at most.
 //
 // A half-warp owns a token's heads of a group, 8 channels a lane: one 16- or 32-byte
 // load and store a head, the sum of squares over 16 lanes, and a pair's other channel
