@@ -408,7 +408,7 @@ typedef struct {
  *              value heads of 128.  row_stride >= (n_q_heads + 2 n_kv_heads) * 128, a multiple of 16 bytes
  *   positions: int32 [n_axes][n_tok], any values (a draft's is its depth, not its slot); NULL if rotary_dim is 0
  *   w_q, w_k:  float [128] or NULL: no norm of the queries, of the keys
- *   eps:       >= 0, finite
+ *   eps:       >= 0, finite.  Heads of any finite size: where squares leave fp32's range they are taken a power of two away
  *   q [n_tok][n_q_heads][128], k, v [n_tok][n_kv_heads][128] of dtype (written; none overlaps qkv).  v NULL: not copied
  * n_q_heads or n_kv_heads may be 0 (cross attention projects them apart). */
 kvq_status kvq_norm_rope(int n_tok, int n_q_heads, int n_kv_heads, const void* qkv, kvq_dtype dtype, int64_t row_stride,

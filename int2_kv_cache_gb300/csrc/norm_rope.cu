@@ -26,6 +26,7 @@ namespace kvq {
 
 constexpr int NR_THREADS = 256;
 constexpr int NR_TOKENS = NR_THREADS / 16;  // tokens a block, one a half-warp
+constexpr float NR_LEAST = 0x1p-110f, NR_MOST = 0x1p126f;  // sums of squares that are as exact as their squares
 
 struct NrArgs {
   int n_tok, n_q, n_kv, heads_per_group;
@@ -34,7 +35,7 @@ struct NrArgs {
   const int32_t* pos;
   const float* w_q;
   const float* w_k;
-  float eps;
+  float eps, least;  // sums of squares below `least` have lost bits that eps does not hide
   bool wide;
   void* out[3];
   RopeDev rope;
@@ -115,9 +116,11 @@ __global__ void __launch_bounds__(NR_THREADS, 5) norm_rope_kernel(const __grid_c
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int AHEAD = F32 ? 2 : 4;  // heads whose loads are in flight
   __shared__ float2 turn[NR_TOKENS][D / 2];  // (cos, sin)
+  __shared__ bool s_odd[NR_TOKENS];          // some head's squares leave fp32's range (the token's 16 lanes agree)
   const int tid = threadIdx.x, l = tid & 15;
   const int tok0 = blockIdx.x * NR_TOKENS, slot = tid >> 4;
   const int half = a.rope.dim / 2;
+  if (tid < NR_TOKENS) s_odd[tid] = false;
 
   {
     const int pair = tid & 63;
@@ -182,6 +185,7 @@ __global__ void __launch_bounds__(NR_THREADS, 5) norm_rope_kernel(const __grid_c
           for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
 #pragma unroll
           for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(FULL, s, d);
+          if (__builtin_expect(!(s >= a.least && s <= NR_MOST), 0)) s_odd[slot] = true;
           r = rsqrtf(fmaf(s, 1.f / D, a.eps));
         }
         if constexpr (SIDE) {
@@ -197,6 +201,47 @@ __global__ void __launch_bounds__(NR_THREADS, 5) norm_rope_kernel(const __grid_c
         for (int i = 0; i < 8; ++i) y[i] = (turned ? fmaf(p[i], B[i], x[i] * A[i]) : x[i] * A[i]) * r;
         if (live) nr_store<F32>(out, ((size_t)t * n + (h + k - first)) * D + 8 * l, nr_pack<F32>(y), a.wide);
       }
+    }
+  }
+  // These heads once more, a power of two smaller or larger.  Behind the loops, out of their registers (in
+  // them: 72 -> 80 us; looking for such heads is 1.1 of 73).
+  __syncwarp();
+  if (__builtin_expect(s_odd[slot], 0)) {
+    const unsigned lanes16 = 0xffffu << (tid & 16);
+#pragma unroll 1
+    for (int h = h0; h < min(h1, a.n_q + a.n_kv); ++h) {
+      const int part = h >= a.n_q, n = part ? a.n_kv : a.n_q;
+      const float* w = part ? a.w_k : a.w_q;
+      if (!w) continue;
+      float x[8], s = 0.f;
+      nr_unpack<F32>(nr_load<F32>(a.qkv, row + (size_t)h * D, a.wide), x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+      for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(lanes16, s, d);
+      if (s >= a.least && s <= NR_MOST) continue;
+      const float c = s < a.least ? 0x1p90f : 0x1p-70f;
+      s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] *= c;
+        s = fmaf(x[i], x[i], s);
+      }
+      for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(lanes16, s, d);
+      const float r = rsqrtf(fmaf(s, 1.f / D, a.eps * c * c));
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int ch = 8 * l + i, o = SIDE ? ch ^ 1 : ch + 8 * other;
+        const float p = SIDE ? x[i ^ 1] : __shfl_sync(lanes16, x[i], l + other, 16);
+        y[i] = x[i] * __ldg(w + ch);
+        if (turned) {
+          float2 cs = turn[ts][SIDE ? ch / 2 : ch - (l < lanes ? 0 : half)];
+          if (SIDE ? (i & 1) == 0 : l < lanes) cs.y = -cs.y;
+          y[i] = fmaf(p, cs.y * __ldg(w + o), x[i] * (cs.x * __ldg(w + ch)));
+        }
+        y[i] *= r;
+      }
+      if (live) nr_store<F32>(a.out[part], ((size_t)t * n + (h - (part ? a.n_q : 0))) * D + 8 * l, nr_pack<F32>(y), a.wide);
     }
   }
   const int first = a.n_q + a.n_kv;
@@ -217,7 +262,7 @@ cudaError_t launch_norm_rope(int n_tok, int n_q_heads, int n_kv_heads, const voi
   const int per = blocks * ((heads + 23) / 24) >= 4ll * device_sm_count() ? 24 : 4;
   const uintptr_t low = reinterpret_cast<uintptr_t>(qkv) | reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
                         reinterpret_cast<uintptr_t>(v) | (uintptr_t)(stride * 4);
-  NrArgs a{n_tok, n_q_heads, n_kv_heads, per, qkv, stride, pos, w_q, w_k, eps, (low & 31) == 0, {q, k, v}, rope};
+  NrArgs a{n_tok, n_q_heads, n_kv_heads, per, qkv, stride, pos, w_q, w_k, eps, eps < NR_LEAST ? NR_LEAST : 0.f, (low & 31) == 0, {q, k, v}, rope};
   const dim3 grid((unsigned)blocks, (unsigned)((heads + per - 1) / per));
   if (dtype == KVQ_F32) {
     if (rope.side) norm_rope_kernel<true, true><<<grid, NR_THREADS, 0, s>>>(a);
