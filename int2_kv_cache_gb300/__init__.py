@@ -525,7 +525,7 @@ def kvq_norm_rope(qkv, positions, rope: Rope, w_q, w_k, eps: float, q, k, v, str
         raise ValueError(f"qkv is on {qkv.device}, not on the current CUDA device")
     if qkv.stride(1) != 1 and n * width > 0:
         raise ValueError("the rows of qkv must be contiguous")
-    stride = qkv.stride(0) if n > 1 else max(qkv.stride(0), width)
+    stride = qkv.stride(0) if n > 1 else width  # a single row's is not used
     if stride < width:
         raise ValueError(f"the rows of qkv overlap (stride {stride}, {width} elements)")
     f32 = torch.float32
