@@ -425,7 +425,8 @@ kvq_status kvq_norm_rope(int n_tok, int n_q_heads, int n_kv_heads, const void* q
  *   start_pos: int32 [n_seqs]
  *   mu_k:      float [n_kv_heads][128], the unrotated key mean, or NULL
  *   k, v:      [n_tok_total][n_kv_heads][128] of dtype (written), each may be NULL, not both
- * fp32 results are within 2^-18 of a row's 2-norm, bf16 ones rounded once from them.  Rows on pages or positions out of
+ * fp32 results are within 2^-18 of the larger of a row's 2-norm in the rotated basis and |z| + 3 |s|, with |mu_k| added, and
+ * bf16 ones rounded once from them.  Rows on pages or positions out of
  * range are flagged (kvq_device_check) and keep their content.  n_tok_total <= 2^31 - 257. */
 kvq_status kvq_read_cache(const kvq_layout* layout, int n_seqs, int n_tok_total, const int32_t* cu_tok,
                           const int32_t* start_pos, const int32_t* block_table, kvq_rot rot_k, kvq_rot rot_v,
@@ -448,8 +449,11 @@ typedef struct {
 
 /* kvq_decode_attention with kvq_score: one query a sequence, at position seq_lens[b] - 1.  Pages that it does not see are
  * not read and their block-table entries may be anything.  Arguments, workspace (kvq_decode_workspace_size with
- * n_splits = 0), limits and errors as there; max_seq_len <= 2^31 - 257, a length above max_seq_len is flagged.  Readouts are about 10^-6 of the
- * values' size off (kvq_decode_attention: 10^-5). */
+ * n_splits = 0), limits and errors as there; max_seq_len <= 2^31 - 257, a length above max_seq_len is flagged.  A page
+ * out of range is flagged and its tokens are not seen; a length out of range is flagged and its output unspecified.
+ * Readouts are about 10^-6 of the values' size off (kvq_decode_attention: 10^-5), at any scale of keys, values and queries
+ * whose rotation stays within fp32; uncapped scores beyond 2^126 are taken as that.  Without modifiers kvq_decode_attention
+ * computes the same at that error, a third faster; it also has the windows (kvq_window) and the step's append. */
 kvq_status kvq_decode_attention_score(const kvq_layout* layout, int n_seqs, const void* q, kvq_dtype q_dtype,
                                       const int32_t* seq_lens, int max_seq_len, const int32_t* block_table,
                                       kvq_rot rot_k, const uint8_t* pool, const kvq_score* score, void* workspace,
