@@ -570,6 +570,10 @@ class Score:
     (tokens, 0: no limit), prefix_lens (int32 [n_seqs] on the device, or None)."""
 
     def __init__(self, cap: float = 0.0, slopes=None, window: int = 0, prefix_lens=None):
+        if cap and not ctypes.c_float(cap).value:
+            raise ValueError(f"score cap {cap} is 0 in fp32, which means none")
+        if not -2 ** 31 <= window < 2 ** 31:  # negative ones are refused by the call
+            raise ValueError(f"score window {window} is no int32")
         self.cap, self.slopes, self.window, self.prefix_lens = cap, slopes, window, prefix_lens
 
     def c(self, layout: KvqLayout, n_seqs: int, dev: int) -> KvqScore:
