@@ -8,7 +8,7 @@
 // is a [128 tokens x 128] x [128 x 128] product whose A operand comes from 32 bytes of
 // codes a row, so scale and zero are applied to the accumulators.  A dense R enters as
 // two fp16 limbs (hi, and the remainder) of R 2^e, e putting its largest element at
-// 2^14: 22 bits and more, as fp32 has to be met.  A Hadamard matrix is +-1, exact in
+// 2^13 to 2^14: 22 bits and more, as fp32 has to be met.  A Hadamard matrix is +-1, exact in
 // one limb with the signs; 1 / sqrt(128) is a factor of the result.
 // The order of the channels inside the product is free as long as codes and R agree on
 // it: a 32-bit word's fields f of both halves (channels 16 w + f and 16 w + 8 + f) go
