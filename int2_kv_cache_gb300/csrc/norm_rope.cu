@@ -16,9 +16,9 @@
 // same lane.  cos and sin are taken once a token (64 of each, shared by its heads),
 // multiplied by the weights once a token and group.
 // Bound: HBM, each element read and written once: 16,384 tokens of 32 / 8 heads in bf16 take
-// 71.6 us, 5.6 TB/s (a plain copy of as many bytes 6.2), 7,777 of 16 / 4 in fp32 35.5, 5.4.
-// Five blocks an SM of 256 threads with four heads' loads in flight: four 73.7, six 84 us; two
-// or eight heads in flight 94 and 92.
+// 72.7 us, 5.5 TB/s (a plain copy of as many bytes 6.2), 7,777 of 16 / 4 in fp32 36.9, 5.2.
+// Five blocks an SM of 256 threads with four heads' loads in flight: four 2 us more, six 12; two
+// or eight heads in flight 22 and 20.
 #include "async_copy.cuh"
 #include "kvq_internal.cuh"
 
@@ -26,7 +26,8 @@ namespace kvq {
 
 constexpr int NR_THREADS = 256;
 constexpr int NR_TOKENS = NR_THREADS / 16;  // tokens a block, one a half-warp
-constexpr float NR_LEAST = 0x1p-110f, NR_MOST = 0x1p126f;  // sums of squares that are as exact as their squares
+constexpr float NR_LEAST = 0x1p-110f, NR_MOST = 0x1p126f;  // sums of squares that are as exact as their squares; below, an eps
+                                                          // of as much hides what they lost
 
 struct NrArgs {
   int n_tok, n_q, n_kv, heads_per_group;
@@ -35,7 +36,7 @@ struct NrArgs {
   const int32_t* pos;
   const float* w_q;
   const float* w_k;
-  float eps, least;  // sums of squares below `least` have lost bits that eps does not hide
+  float eps;
   bool wide;
   void* out[3];
   RopeDev rope;
@@ -110,17 +111,62 @@ __device__ __forceinline__ NrRaw<F32> nr_pack(const float (&x)[8]) {
   return r;
 }
 
+// The heads of this thread's token whose squares leave fp32's range, once more, a power of two smaller or larger.  Out of line,
+// out of the loops' registers (in them: 16,384 tokens 72 -> 80 us; looking for such heads is 0.9 of 73).
+template <bool F32, bool SIDE>
+__device__ __noinline__ void nr_again(const NrArgs& a, const float2 (*turn)[D / 2]) {
+  const int tid = threadIdx.x, l = tid & 15, tok0 = blockIdx.x * NR_TOKENS, slot = tid >> 4, half = a.rope.dim / 2;
+  const unsigned lanes16 = 0xffffu << (tid & 16);
+  const int t = min(tok0 + slot, a.n_tok - 1), heads = a.n_q + a.n_kv, h0 = blockIdx.y * a.heads_per_group;
+  const int lanes = half / 8, other = SIDE || l >= 2 * lanes ? 0 : l < lanes ? lanes : -lanes;
+#pragma unroll 1
+  for (int h = h0; h < min(heads, h0 + a.heads_per_group); ++h) {
+    const int part = h >= a.n_q, n = part ? a.n_kv : a.n_q;
+    const float* w = part ? a.w_k : a.w_q;
+    if (!w) continue;
+    float x[8], s = 0.f;
+    nr_unpack<F32>(nr_load<F32>(a.qkv, (size_t)t * a.stride + 8 * l + (size_t)h * D, a.wide), x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+    for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(lanes16, s, d);
+    const bool small = s < NR_LEAST && a.eps < NR_LEAST;
+    if (!small && s <= NR_MOST) continue;
+    const float c = small ? 0x1p90f : 0x1p-70f;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] *= c;
+      s = fmaf(x[i], x[i], s);
+    }
+    for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(lanes16, s, d);
+    const float r = rsqrtf(fmaf(s, 1.f / D, a.eps * c * c));
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int ch = 8 * l + i, o = SIDE ? ch ^ 1 : ch + 8 * other;
+      const float p = SIDE ? x[i ^ 1] : __shfl_sync(lanes16, x[i], l + other, 16);
+      y[i] = x[i] * __ldg(w + ch);
+      if (l < 2 * lanes) {
+        float2 cs = turn[t - tok0][SIDE ? ch / 2 : ch - (l < lanes ? 0 : half)];
+        if (SIDE ? (i & 1) == 0 : l < lanes) cs.y = -cs.y;
+        y[i] = fmaf(p, cs.y * __ldg(w + o), x[i] * (cs.x * __ldg(w + ch)));
+      }
+      y[i] *= r;
+    }
+    if (tok0 + slot < a.n_tok)
+      nr_store<F32>(a.out[part], ((size_t)t * n + (h - (part ? a.n_q : 0))) * D + 8 * l, nr_pack<F32>(y), a.wide);
+  }
+}
+
 // Grid (token blocks, head groups).  SIDE: pairs (2i, 2i + 1), else (i, i + r / 2).
 template <bool F32, bool SIDE>
 __global__ void __launch_bounds__(NR_THREADS, 5) norm_rope_kernel(const __grid_constant__ NrArgs a) {
   constexpr unsigned FULL = 0xffffffffu;
   constexpr int AHEAD = F32 ? 2 : 4;  // heads whose loads are in flight
   __shared__ float2 turn[NR_TOKENS][D / 2];  // (cos, sin)
-  __shared__ bool s_odd[NR_TOKENS];          // some head's squares leave fp32's range (the token's 16 lanes agree)
   const int tid = threadIdx.x, l = tid & 15;
   const int tok0 = blockIdx.x * NR_TOKENS, slot = tid >> 4;
   const int half = a.rope.dim / 2;
-  if (tid < NR_TOKENS) s_odd[tid] = false;
 
   {
     const int pair = tid & 63;
@@ -148,6 +194,7 @@ __global__ void __launch_bounds__(NR_THREADS, 5) norm_rope_kernel(const __grid_c
   const int other = SIDE || l >= 2 * lanes ? 0 : l < lanes ? lanes : -lanes;
   const bool turned = l < 2 * lanes;
 
+  float odd = 0.f;  // not finite where some head's squares may have left fp32's range (the token's 16 lanes agree)
 #pragma unroll 1
   for (int part = 0; part < 2; ++part) {
     const int first = part ? a.n_q : 0, n = part ? a.n_kv : a.n_q;
@@ -185,8 +232,8 @@ __global__ void __launch_bounds__(NR_THREADS, 5) norm_rope_kernel(const __grid_c
           for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
 #pragma unroll
           for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(FULL, s, d);
-          if (__builtin_expect(!(s >= a.least && s <= NR_MOST), 0)) s_odd[slot] = true;
           r = rsqrtf(fmaf(s, 1.f / D, a.eps));
+          odd = fmaf(r, 0x1p75f, odd + s);
         }
         if constexpr (SIDE) {
 #pragma unroll
@@ -203,47 +250,7 @@ __global__ void __launch_bounds__(NR_THREADS, 5) norm_rope_kernel(const __grid_c
       }
     }
   }
-  // These heads once more, a power of two smaller or larger.  Behind the loops, out of their registers (in
-  // them: 72 -> 80 us; looking for such heads is 1.1 of 73).
-  __syncwarp();
-  if (__builtin_expect(s_odd[slot], 0)) {
-    const unsigned lanes16 = 0xffffu << (tid & 16);
-#pragma unroll 1
-    for (int h = h0; h < min(h1, a.n_q + a.n_kv); ++h) {
-      const int part = h >= a.n_q, n = part ? a.n_kv : a.n_q;
-      const float* w = part ? a.w_k : a.w_q;
-      if (!w) continue;
-      float x[8], s = 0.f;
-      nr_unpack<F32>(nr_load<F32>(a.qkv, row + (size_t)h * D, a.wide), x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-      for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(lanes16, s, d);
-      if (s >= a.least && s <= NR_MOST) continue;
-      const float c = s < a.least ? 0x1p90f : 0x1p-70f;
-      s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] *= c;
-        s = fmaf(x[i], x[i], s);
-      }
-      for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(lanes16, s, d);
-      const float r = rsqrtf(fmaf(s, 1.f / D, a.eps * c * c));
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int ch = 8 * l + i, o = SIDE ? ch ^ 1 : ch + 8 * other;
-        const float p = SIDE ? x[i ^ 1] : __shfl_sync(lanes16, x[i], l + other, 16);
-        y[i] = x[i] * __ldg(w + ch);
-        if (turned) {
-          float2 cs = turn[ts][SIDE ? ch / 2 : ch - (l < lanes ? 0 : half)];
-          if (SIDE ? (i & 1) == 0 : l < lanes) cs.y = -cs.y;
-          y[i] = fmaf(p, cs.y * __ldg(w + o), x[i] * (cs.x * __ldg(w + ch)));
-        }
-        y[i] *= r;
-      }
-      if (live) nr_store<F32>(a.out[part], ((size_t)t * n + (h - (part ? a.n_q : 0))) * D + 8 * l, nr_pack<F32>(y), a.wide);
-    }
-  }
+  if (__builtin_expect(!(odd < INFINITY), 0)) nr_again<F32, SIDE>(a, turn);
   const int first = a.n_q + a.n_kv;
   if (!live || !a.out[2]) return;
 #pragma unroll 4
@@ -262,7 +269,7 @@ cudaError_t launch_norm_rope(int n_tok, int n_q_heads, int n_kv_heads, const voi
   const int per = blocks * ((heads + 23) / 24) >= 4ll * device_sm_count() ? 24 : 4;
   const uintptr_t low = reinterpret_cast<uintptr_t>(qkv) | reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
                         reinterpret_cast<uintptr_t>(v) | (uintptr_t)(stride * 4);
-  NrArgs a{n_tok, n_q_heads, n_kv_heads, per, qkv, stride, pos, w_q, w_k, eps, eps < NR_LEAST ? NR_LEAST : 0.f, (low & 31) == 0, {q, k, v}, rope};
+  NrArgs a{n_tok, n_q_heads, n_kv_heads, per, qkv, stride, pos, w_q, w_k, eps, (low & 31) == 0, {q, k, v}, rope};
   const dim3 grid((unsigned)blocks, (unsigned)((heads + per - 1) / per));
   if (dtype == KVQ_F32) {
     if (rope.side) norm_rope_kernel<true, true><<<grid, NR_THREADS, 0, s>>>(a);
