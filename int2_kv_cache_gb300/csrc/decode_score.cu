@@ -68,11 +68,13 @@ __host__ __device__ constexpr int ds_columns(int gqa, int warps) {
 constexpr int DS_WARP_SMEM = DS_STAGES * 64 * 72;
 
 // How far a half word's field f (bits 2 f, 2 f + 1) is shifted up, and the bit at which it is then masked: 4, 6 or 8 for
-// keys, 7 or 9 for values.
+// keys, 7 or 9 for values, 9 for all of them where few warps are at work (fine).
 __host__ __device__ constexpr int ds_key_shift(int f) { return f < 2 ? 6 : f < 5 ? 0 : -6; }
-__host__ __device__ constexpr int ds_value_shift(int f) { return f == 0 ? 9 : f <= 2 ? 5 : f <= 4 ? 1 : f <= 6 ? -3 : -5; }
+__host__ __device__ constexpr int ds_value_shift(int f, bool fine) {
+  return fine || f == 0 ? 9 - 2 * f : f <= 2 ? 5 : f <= 4 ? 1 : f <= 6 ? -3 : -5;
+}
 __host__ __device__ constexpr int ds_key_bit(int f) { return 2 * f + ds_key_shift(f); }
-__host__ __device__ constexpr int ds_value_bit(int f) { return 2 * f + ds_value_shift(f); }
+__host__ __device__ constexpr int ds_value_bit(int f, bool fine) { return 2 * f + ds_value_shift(f, fine); }
 
 struct DsWs {
   float* part;      // [warps + units][gqa][132]: the partial of warp w for unit u at w + u
@@ -134,6 +136,9 @@ __device__ __forceinline__ uint32_t ds_half2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// floor(log2 x) of a normal x (of a subnormal one -127), and 2^e, e in -126 .. 127.
+__device__ __forceinline__ int ds_exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+__device__ __forceinline__ float ds_pow2(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
 __device__ __forceinline__ float ds_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -222,15 +227,17 @@ __global__ void __launch_bounds__(DS_PREP_THREADS) ds_prepare_kernel(const __gri
       const float4 v = reinterpret_cast<const float4*>(qv[j])[lane];
       const float mx = warp_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
       // the largest |q'| 2^e in [2^9, 2^10): 2^4 more at the lowest field stays in fp16
-      const int e = mx > 0.f && mx < INFINITY ? min(100, 9 - ilogbf(mx)) : 0;  // -119 for the largest finite row
-      const float unit = a.score.cap > 0.f ? scalbnf(a.score.inv_cap, min(0, 60 - 16 + e - ilogbf(a.score.inv_cap)))
-                         : e < -50         ? 1.f / DS_FAR
+      const int e = mx > 0.f && mx < INFINITY ? min(100, 9 - ds_exponent(mx)) : 0;  // -119 for the largest finite row
+      const bool far = a.score.cap == 0.f && e < -50;
+      const float unit = a.score.cap > 0.f ? a.score.inv_cap * ds_pow2(min(0, 60 - 16 + e - ds_exponent(a.score.inv_cap)))
+                         : far             ? 1.f / DS_FAR
                                            : 1.f;
       const float tot = warp_sum((v.x * unit + v.y * unit) + (v.z * unit + v.w * unit));
       if (lane == 0) {
         s_exp[j] = e;
-        const float scale = scalbnf(unit, 16 - e);
-        a.ws.qsum[(size_t)u * G + j] = make_float2(a.score.cap == 0.f && e < -50 ? -scale : scale, tot);
+        const int half = (16 - e) / 2;  // 2^(16 - e) alone may pass fp32
+        const float scale = unit * ds_pow2(half) * ds_pow2(16 - e - half);
+        a.ws.qsum[(size_t)u * G + j] = make_float2(far ? -scale : scale, tot);
       }
     }
     __syncthreads();
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(DS_PREP_THREADS) ds_prepare_kernel(const __gri
       const int j = 4 * nt + (g >> 1);
       float v0 = 0.f, v1 = 0.f;
       if (j < G) {
-        const float f = exp2f((float)(s_exp[j] + 8 - ds_key_bit(s)));
+        const float f = ds_pow2(s_exp[j] + 8 - ds_key_bit(s));
         const float x0 = qv[j][32 * t + 16 * rr + s] * f, x1 = qv[j][32 * t + 16 * rr + 8 + s] * f;
         const float2 hf = __half22float2(__floats2half2_rn(x0, x1));
         v0 = g & 1 ? (x0 - hf.x) * DS_LO : hf.x;
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(DS_PREP_THREADS) ds_prepare_kernel(const __gri
 // ---------------------------------------------------------------------------
 // The decode: blocks of `nw` warps, a slice of the batch's entries each.
 // ---------------------------------------------------------------------------
-template <int G, int P>
+template <int G, int P, bool FINE>
 __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const __grid_constant__ DsArgs a) {
   constexpr int NT = ds_tiles(G), MAXW = ds_max_warps(G);
   constexpr int REC = 72 * P, PPE = 64 / P;  // bytes a page record, pages an entry
@@ -476,7 +483,7 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
         float o[16];
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
-          const float up = (float)(1 << (24 - ds_value_bit(f)));
+          const float up = (float)(1 << (24 - ds_value_bit(f, FINE)));
           o[f] = fmaf(fmaf(acc[nt][f][1], 1.f / DS_LO, acc[nt][f][0]), up, zp[nt]);      // channel 8 g + f
           o[8 + f] = fmaf(fmaf(acc[nt][f][3], 1.f / DS_LO, acc[nt][f][2]), up, zp[nt]);  // channel 64 + 8 g + f
         }
@@ -659,8 +666,8 @@ __global__ void __launch_bounds__(ds_max_warps(G) * 32, 1) ds_split_kernel(const
 #pragma unroll
       for (int f = 0; f < 8; ++f) {
         uint32_t c[4];
-        if (u) ds_field<true>(ds_value_shift(f), ds_value_bit(f), w, c);
-        else ds_field<false>(ds_value_shift(f), ds_value_bit(f), w, c);
+        if (u) ds_field<true>(ds_value_shift(f, FINE), ds_value_bit(f, FINE), w, c);
+        else ds_field<false>(ds_value_shift(f, FINE), ds_value_bit(f, FINE), w, c);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) ds_mma(acc[nt][f], c, bp[nt][u][0], bp[nt][u][1]);
       }
@@ -795,12 +802,12 @@ static cudaError_t ds_launch_pdl(K kernel, dim3 grid, int block, int smem, cudaS
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int G, int P>
+template <int G, int P, bool FINE>
 static cudaError_t ds_launch_split(const DsArgs& a, int warps, int nw, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};  // per device
-  cudaError_t e = smem_limit_once(done, ds_split_kernel<G, P>, ds_max_warps(G) * DS_WARP_SMEM);
+  cudaError_t e = smem_limit_once(done, ds_split_kernel<G, P, FINE>, ds_max_warps(G) * DS_WARP_SMEM);
   if (e != cudaSuccess) return e;
-  return ds_launch_pdl(ds_split_kernel<G, P>, dim3(warps / nw), 32 * nw, nw * DS_WARP_SMEM, s, a);
+  return ds_launch_pdl(ds_split_kernel<G, P, FINE>, dim3(warps / nw), 32 * nw, nw * DS_WARP_SMEM, s, a);
 }
 
 template <int G>
@@ -816,7 +823,12 @@ static cudaError_t ds_launch(const DsArgs& a, const void* q, int dtype, RotDev r
   if (e != cudaSuccess) return e;
   // a full wave is one block an SM, whose warps progress together; fewer warps run as blocks of four
   const int nw = warps == sms * ds_max_warps(G) ? ds_max_warps(G) : 4;
-  e = a.g.page_tokens == 16 ? ds_launch_split<G, 16>(a, warps, nw, s) : ds_launch_split<G, 8>(a, warps, nw, s);
+  // Values all at bit 9: 1,000 tokens 9.0e-7 -> 6.2e-7 off fp64, 16 x 16,384 1.1e-6 -> 9.1e-7, for three more shifts a word: 63.65
+  // -> 65.7 us there, 64 ragged sequences 31.2 -> 33.1, 4 x 4,096 (seven warps an SM) 16.65 -> 17.9; nothing where a scheduler
+  // has one warp at most and waits anyway (1,000 tokens 14.5 us either way).
+  const bool fine = warps <= 4 * sms;
+  if (a.g.page_tokens == 16) e = fine ? ds_launch_split<G, 16, true>(a, warps, nw, s) : ds_launch_split<G, 16, false>(a, warps, nw, s);
+  else e = fine ? ds_launch_split<G, 8, true>(a, warps, nw, s) : ds_launch_split<G, 8, false>(a, warps, nw, s);
   if (e != cudaSuccess) return e;
   const int per_unit = (warps + units - 1) / units + 1;
   int join = 1;
