@@ -196,6 +196,7 @@ kvq_status kvq_decode_workspace_size(const kvq_layout* layout, int n_seqs, int m
  * slice order, so the result does not depend on timing.  A sequence of
  * length 0 yields a zero vector.  Out-of-range lengths or block ids are
  * flagged (kvq_device_check) and the affected outputs are unspecified.
+ * Scales and zeros may have any fp16 value; rotated queries are exact up to 10^20 a channel.
  *   q:       [n_seqs][n_q_heads][128] of q_dtype
  *   seq_lens int32 [n_seqs]; max_seq_len (host) >= every seq_lens[b];
  *            n_seqs <= 65535 and n_seqs * n_kv_heads * ceil(max_seq_len / 32) < 2^30
@@ -461,7 +462,8 @@ kvq_status kvq_decode_attention_score(const kvq_layout* layout, int n_seqs, cons
 
 /* kvq_tree_attention of causal chunks (parents NULL) with kvq_score: query i of sequence b, which has n, at position
  * t = seq_lens[b] - n + i.  Pages that no query of the chunk sees are not read and their block-table entries may be anything.
- * Arguments, workspace (kvq_query_block_workspace_size), precision, limits and errors as there. */
+ * Arguments, workspace (kvq_query_block_workspace_size), precision, limits and errors as there.  A row's scores have to stay
+ * within fp32, capped or not. */
 kvq_status kvq_chunk_attention_score(const kvq_layout* layout, int n_seqs, int n_q_total, const void* q, kvq_dtype q_dtype,
                                      const int32_t* cu_q, int max_q, const int32_t* seq_lens, int max_seq_len,
                                      const int32_t* block_table, kvq_rot rot_k, const uint8_t* pool,

@@ -29,14 +29,15 @@
 // change from a lane a token to a lane a column by matrix transposes (shuffles and selections
 // instead: 2 us more).  A weight times its value scale has to fit fp16: the reference that scores
 // are taken from moves when it does not (scales over 512), and lies below the maximum where all
-// scales are tiny (weight_lift); looking at it in every chunk costs 0.4 of 63 us.
+// scales are tiny (weight_lift); looking at it in every chunk costs 0.7 of 60 us on the
+// device (1.3 of 63.7 a call).
 //
 // Bound: a warp's chain of products, fields and weights, four warps a scheduler (58 % of the
-// issue slots; without the work the call takes 39 us, without the copies alone 61, without
-// both 23): 16 x 16,384 tokens, 32 / 8 heads in 59.4 us, 2.5 TB/s of cache.  A
-// cap adds 10 operations a score, and 6 more only where a warp's scores pass 0.8 of it:
-// 61.8 us.  Ragged lengths and windows cost nothing but their entries: 64 sequences of up to
-// 8,192 tokens, 40 / 10 heads, 64 + 1,024 seen, 30.8 us.
+// issue slots; without the work the call took 39 us, without the copies alone 61, without
+// both 23): 16 x 16,384 tokens, 32 / 8 heads in 61.1 us, 2.5 TB/s of cache.  A
+// cap adds 9 operations a score, and 6 more only where a warp's scores pass 0.8 of it:
+// 63.7 us.  Ragged lengths and windows cost nothing but their entries: 64 sequences of up to
+// 8,192 tokens, 40 / 10 heads, 64 + 1,024 seen, 31.1 us.
 #include <type_traits>
 
 #include "async_copy.cuh"
