@@ -265,7 +265,7 @@ cudaError_t launch_norm_rope(int n_tok, int n_q_heads, int n_kv_heads, const voi
   const int heads = n_q_heads + 2 * n_kv_heads;
   const long long blocks = ((long long)n_tok + NR_TOKENS - 1) / NR_TOKENS;
   // 24 heads a group amortise a token's cos and sin; where that leaves SMs idle, four (one batch of loads).  16,384 tokens of 48
-  // heads: 8, 16, 24, 48 heads a group 94, 73.5, 71.6, 77 us
+  // heads: 8, 16, 24, 48 heads a group 94, 73.5, 71.6, 77 us (other head counts not measured: a last group may be short)
   const int per = blocks * ((heads + 23) / 24) >= 4ll * device_sm_count() ? 24 : 4;
   const uintptr_t low = reinterpret_cast<uintptr_t>(qkv) | reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) |
                         reinterpret_cast<uintptr_t>(v) | (uintptr_t)(stride * 4);

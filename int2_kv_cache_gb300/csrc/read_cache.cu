@@ -519,7 +519,7 @@ static cudaError_t rc_launch_rot(RcArgs& a, cudaStream_t s) {
   cudaError_t e = smem_limit_once(done, read_rot_kernel<DENSE, F32>, rc_smem(DENSE));
   if (e != cudaSuccess) return e;
   // the same number of blocks for each head of each role, side by side, so that all heads' rows of a token go out at about
-  // the same time
+  // the same time (rounded down: two roles of 32 heads take 256 of 304 places, of 80 heads 160)
   const int rhs = a.n_roles * a.g.n_kv_heads, tiles = (a.n_total + 127) / 128;
   const int grid = rhs * std::min(tiles, std::max(1, 2 * device_sm_count() / rhs));
   read_rot_kernel<DENSE, F32><<<grid, RC_THREADS, rc_smem(DENSE), s>>>(a);
